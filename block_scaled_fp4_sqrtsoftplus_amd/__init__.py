@@ -7,7 +7,10 @@ stream); every step of the layer runs in the library's HIP kernels.  There is
 no fallback: if the library is missing, importing this package raises.
 
 Entry points mirror the C names: quant_act, route, expert_ffn, layer
-(plus workspace_size and the Layer helper that keeps one workspace).
+(plus workspace_size and the Layer helper that keeps one workspace).  The
+attention operators of include/moe_attn.h are kv_append, attn_decode (and the
+DecodeAttention helper that keeps its workspace) and attn_prefill, with KVCache
+and Rope as handles on a paged cache and a rotation table.
 """
 
 import ctypes
@@ -322,3 +325,7 @@ def layer(cfg: Config, x, weights, w_gate=None, bias=None, token_ids=None, share
     routing = _routing_tensors(cfg.tokens, cfg.top_k, cfg.n_experts, x.device) if want_routing else None
     y = L(x, token_ids, routing=routing)
     return (y, routing) if want_routing else y
+
+
+from .attention import (  # noqa: E402,F401
+    KV_BF16, KV_FP8, DecodeAttention, KVCache, Rope, attn_decode, attn_prefill, attn_workspace_size, kv_append)

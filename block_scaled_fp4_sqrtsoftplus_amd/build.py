@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libmoe_fp4.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.cpp", "quant_act.hip", "route.hip", "expert_gemm.hip", "expert_gemm_nv.hip", "expert_gemm_w4.hip",
-           "bf16_gemm.hip", "combine.hip", "cast_fp8.hip"]
+           "bf16_gemm.hip", "combine.hip", "cast_fp8.hip", "attn_api.cpp", "kv_append.hip", "attn_decode.hip",
+           "attn_prefill.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <new>
 
+#include "attn_internal.h"
 #include "moe_internal.h"
 
 namespace {
@@ -142,6 +143,15 @@ moe_status check_device() {
   }
   return v == 1 ? MOE_OK : MOE_ERR_ARCH;
 }
+
+}  // namespace
+
+namespace moe {
+// the same check for the entry points of include/moe_attn.h
+moe_status device_ok() { return check_device(); }
+}  // namespace moe
+
+namespace {
 
 moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
