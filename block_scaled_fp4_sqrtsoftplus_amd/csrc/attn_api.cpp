@@ -156,6 +156,8 @@ moe_status moe_attn_prefill(const moe_attn_config* cfg, const moe_rows* q, const
   if ((s = check_rows(k, used && cfg->tokens_kv > 0)) != MOE_OK) return s;
   if ((s = check_rows(v, used && cfg->tokens_kv > 0)) != MOE_OK) return s;
   if ((s = check_rows(out, used)) != MOE_OK) return s;
+  // a tile's rows are addressed in 32 bits from its first
+  if (k->stride_token > (1 << 23) || v->stride_token > (1 << 23)) return MOE_ERR_BAD_SHAPE;
   if (used && !cu_q) return MOE_ERR_NULL_ARG;
   if ((reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(cu_k) & 3u) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))

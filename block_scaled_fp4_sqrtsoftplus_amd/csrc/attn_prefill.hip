@@ -91,34 +91,71 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& p, int tile, Seq& s
 // 16-byte chunk c of row r of a K or V tile in LDS: the position inside the row is permuted
 // so that the reads below touch every bank once.  K: a wave reads one chunk
 // of 32 rows.  V: the transposing read takes 4 chunks of 4 rows.
+
+// 16-byte chunk c of row r of a K or V tile in LDS sits at chunk c ^ swz(r) of
+// the row, so that the reads below touch every bank once.  K: 16 lanes read
+// one chunk of 16 rows.  V: the transposing read takes 4 chunks of 4 rows.
+template <int D>
+__device__ __forceinline__ int k_swz(int r) {
+  return D == 64 ? (r >> 1) & 7 : r & 15;
+}
+template <int D>
+__device__ __forceinline__ int v_swz(int r) {
+  return D == 64 ? 4 * ((r >> 1) & 1) : 4 * (r & 3);
+}
 template <int D>
 __device__ __forceinline__ int k_at(int r, int c) {
-  constexpr int C = D / 8;
-  const int x = C == 8 ? (r >> 1) & 7 : r & 15;
-  return (r * C + (c ^ x)) * 16;
+  return (r * (D / 8) + (c ^ k_swz<D>(r))) * 16;
 }
 template <int D>
 __device__ __forceinline__ int v_at(int r, int c) {
-  constexpr int C = D / 8;
-  const int x = C == 8 ? 4 * ((r >> 1) & 1) : 4 * (r & 3);
-  return (r * C + (c ^ x)) * 16;
+  return (r * (D / 8) + (c ^ v_swz<D>(r))) * 16;
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-template <int D, int BN>
-__global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
+// One asynchronous load of 16 bytes per lane from base + off into LDS at byte
+// `to` (wave-uniform) + 16 * lane.  In assembly because the compiler would
+// wait for it before the next LDS read, which never reads what it writes: the
+// pipeline below waits at the end of the step.  (m0 is this instruction's
+// alone: no other of the kernel's uses it.)
+__device__ __forceinline__ void load_lds16(uint32_t to, const char* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(to), "v"(off), "s"(base)
+               : "memory");
+}
+
+// Ends a step: every asynchronous load of this wave has landed and every wave
+// is done with the step's tiles.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The running maximum follows the scores only when one passes it by more than
+// this (base 2): weights then reach 2^kLag, which fp32 sums and bf16's
+// exponent hold as well, and the output is seldom rescaled.
+constexpr float kLag = 8.f;
+
+// SPLIT waves share 32 rows (each has a D / SPLIT slice of both products'
+// columns, and they add their parts of S through LDS); 4 such groups make the
+// workgroup.  OCC: workgroups per CU the registers are held to, in waves per SIMD.
+template <int D, int BN, int SPLIT, int OCC>
+__global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillArgs p) {
   constexpr int BM = 128;
-  constexpr int NF = D / 16;                 // K fragments per 32 keys
-  constexpr int ND = D / 32;                 // column blocks of O
+  constexpr int TH = 256 * SPLIT;
+  constexpr int NF = D / 16 / SPLIT;         // K fragments of a wave per 32 keys
+  constexpr int ND = D / 32 / SPLIT;         // its column blocks of O
   constexpr int NK = BN / 32;                // 32-key tiles per step
   constexpr int C = D / 8;                   // 16-byte chunks per row
-  constexpr int LD = BN * C / 256;           // chunks a thread stages per tensor
+  constexpr int LD = BN * C / TH;           // chunks a thread stages per tensor
   constexpr int TB = BN * D * 2;             // bytes of one tile
-  __shared__ __align__(16) char lds[4 * TB];   // K, K, V, V
+  constexpr int XB = SPLIT > 1 ? 4 * SPLIT * NK * 4096 : 0;   // the waves' parts of S
+  __shared__ __align__(16) char lds[4 * TB + XB];   // K, K, V, V, S
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = wv / SPLIT, part = wv % SPLIT;   // row group, slice of the columns
   const int col = lane & 31, hh = lane >> 5;
 
   // workgroups go to the 8 XCDs in turn: a key-value head stays on one XCD
@@ -163,7 +200,7 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
     const uint16_t* qp = p.q + (s.q0 + tok) * p.q_st + head * p.q_sh;
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-      u32x4 w = *reinterpret_cast<const u32x4*>(qp + 16 * j + 8 * hh);
+      u32x4 w = *reinterpret_cast<const u32x4*>(qp + 16 * (part * NF + j) + 8 * hh);
       w ^= p.q_flip;
       qf[j] = __builtin_bit_cast(bf16x8, w);
     }
@@ -175,46 +212,44 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m = kNoMax, l = 0.f;
 
-  // staging: a thread's chunks of a tile; rows past the last key repeat it
-  // (their weights are zero, and the row is finite)
-  const uint16_t* kb = p.k + s.k0 * p.k_st + h * p.k_sh;
-  const uint16_t* vb = p.v + s.k0 * p.v_st + h * p.v_sh;
-  u32x4 stage[LD];
-  auto fetch = [&](const uint16_t* base, int64_t st, int key0) {
+  // Staging: chunk i of a thread is chunk tid + TH i of the tile, in row
+  // r0 + RS i.  Its place in the row is permuted on the global side, since the
+  // load writes LDS in lane order.  Rows past the last key repeat it (their
+  // weights are zero, and the row is finite).
+  constexpr int RS = TH / C;
+  const char* kb = reinterpret_cast<const char*>(p.k + s.k0 * p.k_st + h * p.k_sh);
+  const char* vb = reinterpret_cast<const char*>(p.v + s.k0 * p.v_st + h * p.v_sh);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  const int r0 = tid / C, c0 = tid % C;
+  auto fetch = [&](int which, int buf, int key0) {   // which: 0 K, 1 V
+    const char* base = which ? vb : kb;
+    const int64_t st = 2 * (which ? p.v_st : p.k_st);
+    const uint32_t to = lds0 + (2 * which + buf) * TB + wv * 1024;
+    const bool whole = key0 + BN <= s.kn;
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const int r = (tid + 256 * i) / C, c = (tid + 256 * i) % C;
-      stage[i] = *reinterpret_cast<const u32x4*>(base + min(key0 + r, s.kn - 1) * st + c * 8);
-    }
-  };
-  auto put_k = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int r = (tid + 256 * i) / C, c = (tid + 256 * i) % C;
-      *reinterpret_cast<u32x4*>(lds + buf * TB + k_at<D>(r, c)) = stage[i];
-    }
-  };
-  auto put_v = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int r = (tid + 256 * i) / C, c = (tid + 256 * i) % C;
-      *reinterpret_cast<u32x4*>(lds + (2 + buf) * TB + v_at<D>(r, c)) = stage[i];
+      const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
+      if (whole)
+        load_lds16(to + i * TH * 16, base + (key0 + RS * i) * st, (uint32_t)(r0 * (int)st + 16 * c));
+      else
+        load_lds16(to + i * TH * 16, base + key0 * st,
+                   (uint32_t)(min(r0 + RS * i, s.kn - 1 - key0) * (int)st + 16 * c));
     }
   };
   const int steps = key_hi > key_lo ? (key_hi - key_lo + BN - 1) / BN : 0;
   if (steps > 0) {
-    fetch(kb, p.k_st, key_lo);
-    put_k(0);
-    fetch(vb, p.v_st, key_lo);
-    put_v(0);
+    fetch(0, 0, key_lo);
+    fetch(1, 0, key_lo);
   }
-  __syncthreads();
+  step_barrier();
   for (int it = 0; it < steps; ++it) {
     const int key0 = key_lo + it * BN;
     const int buf = it & 1;
-    const bool more = it + 1 < steps;
     const bool mine = key0 < any_hi && key0 + BN > any_lo;   // wave-uniform
-    if (more) fetch(kb, p.k_st, key0 + BN);
+    if (it + 1 < steps) {
+      fetch(0, buf ^ 1, key0 + BN);
+      fetch(1, buf ^ 1, key0 + BN);
+    }
     f32x16 sc[NK];
     if (mine) {
 #pragma unroll
@@ -225,14 +260,33 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
         for (int j = 0; j < NF; ++j) {
           const bf16x8 kf = __builtin_bit_cast(
               bf16x8, *reinterpret_cast<const u32x4*>(lds + buf * TB +
-                                                      k_at<D>(32 * t + col, 2 * j + hh)));
+                                                      k_at<D>(32 * t + col, 2 * (part * NF + j) + hh)));
           sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
         }
       }
     }
-    if (more) {
-      put_k(buf ^ 1);
-      fetch(vb, p.v_st, key0 + BN);
+    if constexpr (SPLIT == 2) {
+      float* x = reinterpret_cast<float*>(lds + 4 * TB);
+      if (mine) {
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4*>(x + ((wv * NK + t) * 4 + i / 4) * 256 + lane * 4) =
+                f32x4{sc[t][i], sc[t][i + 1], sc[t][i + 2], sc[t][i + 3]};
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
+      if (mine) {
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(
+                x + (((wv ^ 1) * NK + t) * 4 + i / 4) * 256 + lane * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[t][i + e] += y[e];
+          }
+      }
     }
     if (mine) {
       if (!(key0 >= all_lo && key0 + BN <= all_hi)) {
@@ -251,7 +305,7 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[t][i]);
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       mx *= p.scale2;
-      if (__ballot(mx > m)) {
+      if (__ballot(mx > m + kLag)) {
         const float mn = fmaxf(m, mx);
         const float a = exp2_fast(m - mn);
         m = mn;
@@ -278,7 +332,7 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
           const int half = (lane & 1) * 8;
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
-            const int ch = 4 * d + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+            const int ch = 4 * (part * ND + d) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (lds_s16x4*)(lds + (2 + buf) * TB + v_at<D>(r, ch) + half));
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -290,8 +344,7 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
         }
       }
     }
-    if (more) put_v(buf ^ 1);
-    __syncthreads();
+    step_barrier();
   }
 
   l += __shfl_xor(l, 32);
@@ -304,9 +357,9 @@ __global__ __launch_bounds__(256) void attn_prefill_kernel(PrefillArgs p) {
     for (int i = 0; i < 16; i += 4) {
       const u32x2 w = {pack_bf16(o[d][i] * inv, o[d][i + 1] * inv),
                        pack_bf16(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-      *reinterpret_cast<u32x2*>(dst + 32 * d + 2 * i + 4 * hh) = w;
+      *reinterpret_cast<u32x2*>(dst + 32 * (part * ND + d) + 2 * i + 4 * hh) = w;
     }
-  if (p.lse && hh == 0)
+  if (p.lse && hh == 0 && part == 0)
     p.lse[(int64_t)(s.q0 + tok) * p.hq + head] =
         l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
@@ -333,13 +386,19 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
   const int64_t tiles =
       c.tokens * a.group / 128 + std::min<int64_t>(c.batch, c.tokens);
   const dim3 grid((unsigned)(tiles * c.heads_kv));
+#define MOE_PREFILL(D, BN, SPLIT, OCC)                                                        \
+  case D:                                                                                     \
+    hipLaunchKernelGGL((attn_prefill_kernel<D, BN, SPLIT, OCC>), grid, dim3(256 * SPLIT), 0, st, \
+                       a);                                                                    \
+    break;
   switch (c.head_dim) {
-    case 64: hipLaunchKernelGGL((attn_prefill_kernel<64, 64>), grid, dim3(256), 0, st, a); break;
-    case 128: hipLaunchKernelGGL((attn_prefill_kernel<128, 64>), grid, dim3(256), 0, st, a); break;
-    case 256: hipLaunchKernelGGL((attn_prefill_kernel<256, 32>), grid, dim3(256), 0, st, a); break;
-    case 512: hipLaunchKernelGGL((attn_prefill_kernel<512, 32>), grid, dim3(256), 0, st, a); break;
+    MOE_PREFILL(64, 64, 1, 2)
+    MOE_PREFILL(128, 64, 1, 2)
+    MOE_PREFILL(256, 32, 1, 1)
+    MOE_PREFILL(512, 32, 2, 2)
     default: return hipErrorInvalidValue;
   }
+#undef MOE_PREFILL
   return hipGetLastError();
 }
 

@@ -148,7 +148,8 @@ moe_status moe_attn_decode(const moe_attn_config* cfg, const moe_rows* q,
  * with a context before it has more keys than queries; with fewer keys the first rows keep nothing.
  *   cu_q, cu_k   [batch + 1] int32, not decreasing (entries are clamped to
  *                [0, tokens] and [0, tokens_kv]); cu_k NULL: cu_q
- *   k, v         [tokens_kv, heads_kv, head_dim]; v may be k
+ *   k, v         [tokens_kv, heads_kv, head_dim], stride_token at most 2^23;
+ *                v may be k
  *   lse          [tokens, heads_q] fp32 or NULL
  * Rows of q that belong to no sequence are left as they are in out and lse. */
 moe_status moe_attn_prefill(const moe_attn_config* cfg, const moe_rows* q, const moe_rows* k,

@@ -129,7 +129,7 @@ def _prefill(cfg=None, q=None, k=None, v=None, cu_q=16, cu_k=None, out=None, lse
     (SHAPE, dict(cfg=_cfg(causal=2))), (SHAPE, dict(cfg=_cfg(tokens_kv=-1))), (SHAPE, dict(cfg=_cfg(tokens_kv=1 << 30))),
     (NULL, dict(cu_q=None)), (ALIGN, dict(cu_q=18)), (ALIGN, dict(cu_k=18)), (ALIGN, dict(lse=6)),
     (NULL, dict(k=_rows(p=None))), (NULL, dict(out=_rows(p=None))), (ALIGN, dict(v=_rows(p=8))),
-    (ALIGN, dict(q=_rows(stride_token=12))),
+    (ALIGN, dict(q=_rows(stride_token=12))), (SHAPE, dict(k=_rows(stride_token=(1 << 23) + 8))),
 ])
 def test_prefill_refusals(status, kw):
     assert _prefill(**kw) == status
