@@ -38,6 +38,7 @@ moe_status check_cache(const moe_kv_cache* c) {
       !stride_ok(c->stride_token, 1))
     return MOE_ERR_BAD_SHAPE;
   const int64_t unit = c->format == MOE_KV_FP8 ? 16 : 8;
+  if (c->stride_token > (1 << 23)) return MOE_ERR_BAD_SHAPE;   // rows of a tile: 32-bit offsets
   if (c->stride_page % unit || c->stride_head % unit || c->stride_token % unit)
     return MOE_ERR_MISALIGNED;
   if (c->pages > 0) {

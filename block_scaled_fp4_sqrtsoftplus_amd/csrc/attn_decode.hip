@@ -29,7 +29,9 @@ namespace moe {
 namespace {
 
 constexpr int kTileKeys = 128;     // unit of the split over a sequence's keys
-constexpr int kSplitTarget = 1024; // workgroups the tiles are dealt to
+// Workgroups the tiles are dealt to, by the kernel that takes them.
+constexpr int kSplitTarget = 1024;
+constexpr int kSplitTargetRows = 256;
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -55,6 +57,11 @@ struct DecodeArgs {
   float* part_l;           // ... and sum
   int2* meta;              // [batch] first slot, splits
 };
+
+// An entry of a table that no kernel writes, at a wave-uniform index: a scalar load.
+__device__ __forceinline__ int entry(const int32_t* t, int64_t i) {
+  return *(const __attribute__((address_space(4))) int32_t*)(t + i);
+}
 
 // Keys a sequence's rows may reach: [lo, len), and how many 128-key tiles
 // that is, counted from lo rounded down to a step of 32.
@@ -135,11 +142,76 @@ __device__ __forceinline__ u32x2 fp8x4_to_bf16(uint32_t w, float s) {
   return r;
 }
 
-// D: head size; RT: 16-row tiles of a workgroup, one per wave (1, 2 or 4);
-// the 4 / RT waves of one tile take every (4 / RT)th step of 32 keys.
-template <int D, bool FP8, int RT>
+// Joins the KP waves that share a row tile (rt of RT): half of them hand their
+// maximum, sum and NQ quads to the others through LDS, until wave 0 has all.
+// lds: RT * KP / 2 * (NQ * 256 + 128) floats.
+template <int KP, int RT, int NQ>
+__device__ __forceinline__ void join_waves(float* lds, int kp, int rt, float& m, float& l,
+                                           f32x4* o) {
+  constexpr int SZ = NQ * 256 + 128;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int half = KP / 2; half >= 1; half >>= 1) {
+    if (kp >= half && kp < 2 * half) {
+      float* to = lds + (rt * (KP / 2) + kp - half) * SZ;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) *reinterpret_cast<f32x4*>(to + (i * 64 + lane) * 4) = o[i];
+      to[NQ * 256 + lane] = m;
+      to[NQ * 256 + 64 + lane] = l;
+    }
+    __syncthreads();
+    if (kp < half) {
+      const float* from = lds + (rt * (KP / 2) + kp) * SZ;
+      const float m2 = from[NQ * 256 + lane], l2 = from[NQ * 256 + 64 + lane];
+      const float mn = fmaxf(m, m2);
+      const float a = exp2_fast(m - mn), c = exp2_fast(m2 - mn);
+      m = mn;
+      l = l * a + l2 * c;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+        o[i] = o[i] * a + *reinterpret_cast<const f32x4*>(from + (i * 64 + lane) * 4) * c;
+    }
+    __syncthreads();
+  }
+}
+
+// Writes a row tile's result: the output where its sequence has one split,
+// else the split's partial result.  A lane has NQ quads of its row: columns
+// col(i) .. + 3, values val(i).
+template <int D, int NQ, class Col, class Val>
+__device__ __forceinline__ void finish(const DecodeArgs& p, const Piece& pc, int slot, int h, int rg,
+                                       int row, bool row_live, int64_t qrow, int head, int g,
+                                       float m, float l, Col col, Val val) {
+  if (pc.split == 0 && h == 0 && rg == 0 && threadIdx.x == 0)
+    p.meta[pc.b] = make_int2(pc.slot0, pc.splits);
+  if (!row_live) return;
+  if (pc.splits == 1) {
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    uint16_t* dst = p.out + qrow * p.o_st + head * p.o_sh;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const f32x4 x = val(i) * inv;
+      *reinterpret_cast<u32x2*>(dst + col(i)) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    }
+    if (p.lse && g == 0)
+      p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+  } else {
+    const int64_t idx = ((int64_t)slot * p.hkv + h) * p.rows + row;
+    float* dst = p.part_o + idx * D;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) *reinterpret_cast<f32x4*>(dst + col(i)) = val(i);
+    if (g == 0) {
+      p.part_m[idx] = m;
+      p.part_l[idx] = l;
+    }
+  }
+}
+
+// Up to 16 rows for a key-value head: each of 4 waves takes every fourth step of 32 keys,
+// from memory to registers.
+template <int D, bool FP8>
 __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
-  constexpr int KP = 4 / RT;
+  constexpr int KP = 4;
   constexpr int NF = D / 32;                  // K fragments per 16-key tile
   constexpr int DV = D < 128 ? D / 16 : 8;    // columns of V per lane and block
   constexpr int NB = D / (16 * DV);           // blocks of 16 * DV columns
@@ -149,21 +221,20 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int rt = wave % RT, kp = wave / RT;
+  const int kp = wave;
 
-  const int per_slot = p.hkv * p.rgroups;
-  const int slot = blockIdx.x / per_slot;
-  const int rest = blockIdx.x - slot * per_slot;
-  const int rg = rest / p.hkv, h = rest - rg * p.hkv;
+  const int slot = blockIdx.x / p.hkv;
+  const int h = blockIdx.x - slot * p.hkv;
+  constexpr int rg = 0;
   Piece pc;
   if (!find_piece(p, slot, pc)) return;
-  const Range rng = range_of(p, __builtin_amdgcn_readfirstlane(p.seq_lens[pc.b]));
+  const Range rng = range_of(p, entry(p.seq_lens, pc.b));
   const int len = rng.len, lo = rng.lo;
   const int first = (lo & ~31) + pc.split * pc.c * kTileKeys;
   const int last = (int)min((int64_t)len, (int64_t)first + (int64_t)pc.c * kTileKeys);
 
   // this lane's row: token, head and the keys it keeps [row_lo, row_hi)
-  const int row = (rg * RT + rt) * 16 + col;
+  const int row = col;
   const bool row_live = row < p.rows;
   const int tok = row_live ? row / p.group : 0;
   const int head = row_live ? h * p.group + row - tok * p.group : 0;
@@ -203,7 +274,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
     for (int t = 0; t < 2; ++t) {
       const int kt = key0 + 16 * t;
       have[t] = kt < len && kt + 16 > lo;
-      int pid = have[t] ? trow[kt >> p.page_shift] : 0;
+      int pid = have[t] ? entry(trow, kt >> p.page_shift) : 0;
       have[t] = have[t] && pid >= 0 && pid < p.pages;
       pid = have[t] ? pid : 0;
       off[t] = pid * p.sp + (int64_t)(kt & page_mask) * p.st;
@@ -306,7 +377,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
     for (int i = 0; i < 8; ++i) mx = fmaxf(mx, pr[i]);
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
-    if (__ballot(mx > m)) {
+    if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float a = exp2_fast(m - mn);
       m = mn;
@@ -357,129 +428,310 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 
-  // join the waves of one row tile: half of them hand theirs to the others
-  if constexpr (KP > 1) {
-    constexpr int SZ = NB * DV * 4 * 64;        // floats of o per wave
-    __shared__ float lds[RT * (KP / 2) * (SZ + 128)];
-#pragma unroll
-    for (int half = KP / 2; half >= 1; half >>= 1) {
-      if (kp >= half && kp < 2 * half) {
-        float* to = lds + (rt * (KP / 2) + kp - half) * (SZ + 128);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < DV; ++i)
-            *reinterpret_cast<f32x4*>(to + ((b * DV + i) * 64 + lane) * 4) = o[b][i];
-        to[SZ + lane] = m;
-        to[SZ + 64 + lane] = l;
-      }
-      __syncthreads();
-      if (kp < half) {
-        const float* from = lds + (rt * (KP / 2) + kp) * (SZ + 128);
-        const float m2 = from[SZ + lane], l2 = from[SZ + 64 + lane];
-        const float mn = fmaxf(m, m2);
-        const float a = exp2_fast(m - mn), c = exp2_fast(m2 - mn);
-        m = mn;
-        l = l * a + l2 * c;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < DV; ++i) {
-            const f32x4 y = *reinterpret_cast<const f32x4*>(from + ((b * DV + i) * 64 + lane) * 4);
-            o[b][i] = o[b][i] * a + y * c;
-          }
-      }
-      __syncthreads();
-    }
-    if (kp > 0) return;
-  }
+  __shared__ float lds[KP / 2 * (NB * DV * 256 + 128)];
+  join_waves<KP, 1, NB * DV>(lds, kp, 0, m, l, &o[0][0]);
+  if (kp > 0) return;
 
-  if (pc.split == 0 && h == 0 && rg == 0 && threadIdx.x == 0)
-    p.meta[pc.b] = make_int2(pc.slot0, pc.splits);
-  if (!row_live) return;
-  if (pc.splits == 1) {
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    uint16_t* dst = p.out + qrow * p.o_st + head * p.o_sh;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        uint32_t w[DV / 2];
-#pragma unroll
-        for (int i = 0; i < DV / 2; ++i)
-          w[i] = pack_bf16(o[b][2 * i][r] * inv, o[b][2 * i + 1][r] * inv);
-        uint16_t* to = dst + b * 16 * DV + (4 * g + r) * DV;
-        if constexpr (DV == 8)
-          *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
-        else
-          *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
-      }
-    if (p.lse && g == 0)
-      p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-  } else {
-    const int64_t at = ((int64_t)slot * p.hkv + h) * p.rows + row;
-    float* dst = p.part_o + at * D;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < DV; i += 4)
-          *reinterpret_cast<f32x4*>(dst + b * 16 * DV + (4 * g + r) * DV + i) =
-              f32x4{o[b][i][r], o[b][i + 1][r], o[b][i + 2][r], o[b][i + 3][r]};
-    if (g == 0) {
-      p.part_m[at] = m;
-      p.part_l[at] = l;
-    }
-  }
+  // quad i: block b, row r of V's operand, columns 4 c of the lane's DV
+  constexpr int QD = DV / 4;
+  finish<D, NB * 4 * QD>(
+      p, pc, slot, h, rg, row, row_live, qrow, head, g, m, l,
+      [&](int i) { return i / (4 * QD) * 16 * DV + (4 * g + i / QD % 4) * DV + i % QD * 4; },
+      [&](int i) {
+        const int b = i / (4 * QD), r = i / QD % 4, c = i % QD * 4;
+        return f32x4{o[b][c][r], o[b][c + 1][r], o[b][c + 2][r], o[b][c + 3][r]};
+      });
 }
 
-// Joins the splits of a sequence: one wave per (sequence, head, row); rows of a
-// sequence with one split are written already.
+// Position of 16-byte chunk c of row r in an LDS tile whose rows serve as keys
+// (16 lanes read one chunk of 16 rows) and as values (the transposing read
+// takes 2 chunks of 8 rows): both touch every bank once.
+template <int D>
+__device__ __forceinline__ int kv_at(int r, int c) {
+  const int x = D == 64 ? (((r >> 1) & 3) << 1) | ((r >> 3) & 1) : ((r & 7) << 1) | ((r >> 3) & 1);
+  // the permutation stays in 16 chunks, so that the rest is a constant offset
+  return (r * (D / 8) + ((c & 15) ^ x)) * 16 + (c & ~15) * 16;
+}
+
+// More than 16 rows for a key-value head: RT row tiles of 16 (2 or 4), one per
+// wave, share K and V through LDS, and 4 / RT waves share a row tile, 32 keys
+// of a step each.  A step's tiles are loaded while the one before is computed:
+// bf16 straight into LDS, FP8 through registers, turned into bf16 once for all waves.
+// ONE: one tensor serves as keys and values, and is loaded once.
+template <int D, bool FP8, int RT, bool ONE>
+__global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_rows_kernel(
+    DecodeArgs p) {
+  constexpr int KP = 4 / RT;
+  constexpr int KT = 32 * KP;                 // keys per step
+  constexpr int NF = D / 32;
+  constexpr int NB = D / 16;
+  constexpr int C = D / 8;                    // 16-byte bf16 chunks per row
+  constexpr int NG = D < 128 ? 1 : D / 128;
+  constexpr int TB = KT * D * 2;
+  constexpr int NT = ONE ? 1 : 2;
+  constexpr int LD = KT * C / 256;            // chunks a thread stages per tensor
+  constexpr int JOIN = KP > 1 ? RT * (KP / 2) * (NB * 256 + 128) * 4 : 0;
+  constexpr int LDS = 2 * NT * TB > JOIN ? 2 * NT * TB : JOIN;
+  __shared__ __align__(16) char lds[LDS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int rt = wave % RT, kp = wave / RT;
+
+  const int per_slot = p.hkv * p.rgroups;
+  const int slot = blockIdx.x / per_slot;
+  const int rest = blockIdx.x - slot * per_slot;
+  const int rg = rest / p.hkv, h = rest - rg * p.hkv;
+  Piece pc;
+  if (!find_piece(p, slot, pc)) return;
+  const Range rng = range_of(p, entry(p.seq_lens, pc.b));
+  const int len = rng.len, lo = rng.lo;
+  const int first = (lo & ~31) + pc.split * pc.c * kTileKeys;
+  const int last = (int)min((int64_t)len, (int64_t)first + (int64_t)pc.c * kTileKeys);
+
+  const int row = (rg * RT + rt) * 16 + col;
+  const bool row_live = row < p.rows;
+  const int tok = row_live ? row / p.group : 0;
+  const int head = row_live ? h * p.group + row - tok * p.group : 0;
+  const int64_t qrow = (int64_t)pc.b * p.q_len + tok;
+  const int row_hi = len - p.q_len + 1 + tok;
+  const int row_lo = p.window > 0 ? row_hi - p.window : 0;
+  const int all_hi = len - p.q_len + 1;
+  const int all_lo = p.window > 0 ? len - p.window : 0;
+
+  bf16x8 qf[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) {
+    u32x4 w = {0, 0, 0, 0};
+    if (row_live)
+      w = *reinterpret_cast<const u32x4*>(p.q + qrow * p.q_st + head * p.q_sh + 32 * j + 8 * g);
+    qf[j] = __builtin_bit_cast(bf16x8, w);
+  }
+  f32x4 o[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = kNoMax, l = 0.f;
+
+  const int32_t* trow = p.table + (int64_t)pc.b * p.table_width;
+  const int page_mask = (1 << p.page_shift) - 1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  // a wave stages rows wave * KT / 4 .. of a step, in one 16-key tile and so one page
+  constexpr int WR = KT / 4;                  // rows per wave
+  constexpr int RI = WR / LD;                 // rows per load of the wave
+  static_assert(16 % WR == 0 && RI * LD == WR, "a wave's rows stay in one page");
+  const int sr = lane / C % (RI > 0 ? RI : 1), sc = lane % C;
+  // page of the wave's rows, or -1: no key of them is read
+  auto page_at = [&](int key0) {
+    const int kt = (key0 + wave * WR) & ~15;
+    if (!(kt < len && kt + 16 > lo)) return -1;
+    const int pid = entry(trow, kt >> p.page_shift);
+    return pid >= 0 && pid < p.pages ? pid : -1;
+  };
+  u32x2 reg[FP8 ? NT : 1][FP8 ? LD : 1];      // FP8: codes of a step on their way
+  uint32_t rsc[FP8 ? NT : 1][FP8 ? LD : 1];   // and their scale bytes
+  // the chunk of its row that belongs at this lane's place of tile row tr
+  auto chunk = [&](int tr) { return (kv_at<D>(tr, sc) >> 4) - tr * C; };
+  auto fetch = [&](int buf, int key0) {
+    const int pid = page_at(key0);
+    const int kr = key0 + wave * WR;          // the wave's first key
+    const int64_t off = (int64_t)max(pid, 0) * p.sp + h * p.sh + (int64_t)(kr & page_mask) * p.st;
+    const int64_t srow = (((int64_t)max(pid, 0) * p.hkv + h) << p.page_shift) + (kr & page_mask);
+    const int ra = pid >= 0 ? max(lo - kr, 0) : 0;                // rows [ra, rz) are read;
+    const int rz = pid >= 0 ? max(min(len - kr, WR), 0) : 0;      // the others are zeros
+    if constexpr (FP8) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const char* base = (t ? p.v : p.k) + off;
+        const uint8_t* sb = (t ? p.vs : p.ks) + srow * NG;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+          const int r = RI * i + sr;
+          const int c = chunk(wave * WR + r);
+          reg[t][i] = u32x2{0, 0};
+          rsc[t][i] = 127;
+          if (r >= ra && r < rz) {
+            reg[t][i] = *reinterpret_cast<const u32x2*>(base + (uint32_t)(r * (int)p.st + 8 * c));
+            rsc[t][i] = sb[(uint32_t)(r * NG + c / 16)];
+          }
+        }
+      }
+    } else if (ra == 0 && rz == WR) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const char* base = (t ? p.v : p.k) + off;
+        const uint32_t to = lds0 + (2 * t + buf) * TB + wave * WR * D * 2;
+#pragma unroll
+        for (int i = 0; i < LD; ++i)
+          load_lds16(to + RI * i * D * 2, base + RI * i * p.st,
+                     (uint32_t)(sr * (int)p.st + 16 * chunk(wave * WR + RI * i + sr)));
+      }
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < NT * LD; ++j) {
+        const int t = j / LD, i = j % LD;
+        const int r = RI * i + sr;
+        u32x4 w = {0, 0, 0, 0};
+        if (r >= ra && r < rz)
+          w = *reinterpret_cast<const u32x4*>((t ? p.v : p.k) + off + r * p.st +
+                                              16 * chunk(wave * WR + r));
+        *reinterpret_cast<u32x4*>(lds + (2 * t + buf) * TB + (wave * WR + RI * i) * D * 2 +
+                                  lane * 16) = w;
+      }
+    }
+  };
+  auto put = [&](int buf) {                   // FP8: the fetched codes as bf16 into LDS
+    if constexpr (FP8) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+          const float s = scale_of(rsc[t][i]);
+          const u32x2 a = fp8x4_to_bf16(reg[t][i][0], s), b = fp8x4_to_bf16(reg[t][i][1], s);
+          *reinterpret_cast<u32x4*>(lds + (2 * t + buf) * TB + (wave * WR + RI * i) * D * 2 +
+                                    lane * 16) = u32x4{a[0], a[1], b[0], b[1]};
+        }
+    }
+  };
+
+  if (first < last) fetch(0, first);
+  put(0);
+  step_barrier();
+  int buf = 0;
+  for (int key0 = first; key0 < last; key0 += KT, buf ^= 1) {
+    const bool more = key0 + KT < last;
+    if (more) fetch(buf ^ 1, key0 + KT);
+    const int mykey = key0 + 32 * kp;
+    // LDS places of this lane's chunks: kv_at's permutation is an exclusive or,
+    // so chunk 4 j + g (keys) and 2 b + .. (values) are the lane's first one
+    // with the bits of j or b flipped.  Worked out anew in each step: kept
+    // over the loop they would take registers the loop does not have.
+    const int vr = 32 * kp + 4 * g + (col >> 2);
+    int ka = buf * TB + kv_at<D>(32 * kp + col, g);
+    int va = (ONE ? 0 : 2 * TB) + buf * TB + kv_at<D>(vr, (col & 3) >> 1) + (col & 1) * 8;
+    asm volatile("" : "+v"(ka), "+v"(va));
+    if (KP == 1 || mykey < last) {
+      f32x4 s[2];
+      bool have[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int k16 = mykey + 16 * t;
+        have[t] = k16 < len && k16 + 16 > lo;
+        const int pid = have[t] ? entry(trow, k16 >> p.page_shift) : -1;
+        have[t] = pid >= 0 && pid < p.pages;
+        s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const bf16x8 kf = __builtin_bit_cast(
+              bf16x8, *reinterpret_cast<const u32x4*>(lds + (ka ^ ((j & 3) * 64)) +
+                                                      (j >> 2) * 256 + t * 16 * D * 2));
+          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[j], s[t], 0, 0, 0);
+        }
+      float pr[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pr[i] = s[i >> 2][i & 3] * p.scale2;
+      if (!(have[0] && have[1] && mykey >= all_lo && mykey + 32 <= all_hi)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = mykey + 16 * (i >> 2) + 4 * g + (i & 3);
+          if (!(have[i >> 2] && key < row_hi && key >= row_lo)) pr[i] = -INFINITY;
+        }
+      }
+      float mx = pr[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, pr[i]);
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (__ballot(mx > m + kLag)) {
+        const float mn = fmaxf(m, mx);
+        const float a = exp2_fast(m - mn);
+        m = mn;
+        l *= a;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) o[b] *= a;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pr[i] = exp2_fast(pr[i] - m);
+      l += ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
+      const u32x4 pw = {pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3]),
+                        pack_bf16(pr[4], pr[5]), pack_bf16(pr[6], pr[7])};
+      const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const char* v0 = lds + (va ^ ((b & 7) * 32)) + (b >> 3) * 256;
+        const bf16x8 vf = read_tr(v0, v0 + 16 * D * 2);
+        o[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, o[b], 0, 0, 0);
+      }
+    }
+    if (more) put(buf ^ 1);
+    step_barrier();
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if constexpr (KP > 1) {
+    join_waves<KP, RT, NB>(reinterpret_cast<float*>(lds), kp, rt, m, l, o);
+    if (kp > 0) return;
+  }
+  finish<D, NB>(
+      p, pc, slot, h, rg, row, row_live, qrow, head, g, m, l,
+      [&](int i) { return 16 * i + 4 * g; }, [&](int i) { return o[i]; });
+}
+
+// Joins the splits of a sequence: one workgroup per (sequence, head, row);
+// rows of a sequence with one split are written already.  A group of D / 4 lanes takes a split's
+// row, the groups every (1024 / D)th split, and their sums meet in LDS.
 template <int D>
 __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
-  constexpr int EPL = D / 64;     // elements per lane
-  const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  constexpr int GL = D / 4, NGR = 256 / GL;
+  __shared__ f32x4 so[NGR][GL];
+  __shared__ float sl[NGR];
   const int64_t per_b = (int64_t)p.hkv * p.rows;
-  const int64_t b = w / per_b;
-  if (b >= p.batch) return;
-  const int rest = (int)(w - b * per_b);
+  const int64_t b = blockIdx.x / per_b;
+  const int rest = (int)(blockIdx.x - b * per_b);
   const int h = rest / p.rows, row = rest - h * p.rows;
   const int2 mt = p.meta[b];
   if (mt.y <= 1) return;
-  const int64_t stride = (int64_t)p.hkv * p.rows;
-  const int64_t at0 = (int64_t)mt.x * stride + (int64_t)h * p.rows + row;
+  const int64_t at0 = (int64_t)mt.x * per_b + (int64_t)h * p.rows + row;
+  const int lane = threadIdx.x & 63;
+  const int gr = threadIdx.x / GL, gl = threadIdx.x % GL;
   float m = kNoMax;
-  for (int i = lane; i < mt.y; i += 64) m = fmaxf(m, p.part_m[at0 + i * stride]);
+  for (int i = lane; i < mt.y; i += 64) m = fmaxf(m, p.part_m[at0 + i * per_b]);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
-  float l = 0.f, o[EPL];
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  for (int i = 0; i < mt.y; ++i) {
-    const int64_t at = at0 + i * stride;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = gr; i < mt.y; i += NGR) {
+    const int64_t at = at0 + i * per_b;
     const float a = exp2_fast(p.part_m[at] - m);
-    l = fmaf(a, p.part_l[at], l);
+    l += a * p.part_l[at];
+    o += a * *reinterpret_cast<const f32x4*>(p.part_o + at * D + gl * 4);
+  }
+  so[gr][gl] = o;
+  if (gl == 0) sl[gr] = l;
+  __syncthreads();
+  if (gr > 0) return;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] = fmaf(a, p.part_o[at * D + lane * EPL + e], o[e]);
+  for (int i = 1; i < NGR; ++i) {
+    o += so[i][gl];
+    l += sl[i];
   }
   const float inv = l > 0.f ? 1.0f / l : 0.f;
+  o *= inv;
   const int tok = row / p.group;
   const int head = h * p.group + row - tok * p.group;
   const int64_t qrow = b * p.q_len + tok;
-  uint16_t* dst = p.out + qrow * p.o_st + head * p.o_sh + lane * EPL;
-  if constexpr (EPL == 1) {
-    *dst = (uint16_t)(pack_bf16(o[0] * inv, 0.f) & 0xFFFFu);
-  } else {
-#pragma unroll
-    for (int e = 0; e < EPL; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
-  }
-  if (p.lse && lane == 0) p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+  *reinterpret_cast<u32x2*>(p.out + qrow * p.o_st + head * p.o_sh + gl * 4) =
+      u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+  if (p.lse && gl == 0)
+    p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
-int row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Row tiles of a workgroup.  Two tiles leave two waves to share each, which
+// doubles a step's keys: 512-element heads have no LDS for that.
+int row_tiles(int rows, int dim) { return rows <= 16 ? 1 : rows <= 32 && dim < 512 ? 2 : 4; }
 
 struct DecodePlan {
   int rows, rgroups, target, slots;
@@ -487,9 +739,9 @@ struct DecodePlan {
 DecodePlan plan_of(const moe_attn_config& c) {
   DecodePlan d;
   d.rows = c.q_len * (c.heads_q / c.heads_kv);
-  const int rt = row_tiles(d.rows);
+  const int rt = row_tiles(d.rows, c.head_dim);
   d.rgroups = (d.rows + 16 * rt - 1) / (16 * rt);
-  d.target = std::max(1, kSplitTarget / (c.heads_kv * d.rgroups));
+  d.target = std::max(1, (rt == 1 ? kSplitTarget : kSplitTargetRows) / (c.heads_kv * d.rgroups));
   d.slots = d.target + c.batch;
   return d;
 }
@@ -530,32 +782,33 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.part_l = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.meta = reinterpret_cast<int2*>(w);
   const dim3 grid((unsigned)d.slots * c.heads_kv * d.rgroups);
-  const int rt = row_tiles(d.rows);
+  const int rt = row_tiles(d.rows, c.head_dim);
   const bool f8 = kv.format == MOE_KV_FP8;
-#define MOE_DECODE_RT(D, F, R) \
-  hipLaunchKernelGGL((attn_decode_kernel<D, F, R>), grid, dim3(256), 0, st, a)
+  const bool one = kv.k == kv.v;
+#define MOE_ROWS(D, F, R, O) \
+  hipLaunchKernelGGL((attn_decode_rows_kernel<D, F, R, O>), grid, dim3(256), 0, st, a)
+#define MOE_ROWS_F(D, F)                                                                      \
+  do {                                                                                        \
+    if (rt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, F>), grid, dim3(256), 0, st, a);   \
+    else if (rt == 2 && one) MOE_ROWS(D, F, (D < 512 ? 2 : 4), true);                         \
+    else if (rt == 2) MOE_ROWS(D, F, (D < 512 ? 2 : 4), false);                               \
+    else if (one) MOE_ROWS(D, F, 4, true);                                                    \
+    else MOE_ROWS(D, F, 4, false);                                                            \
+  } while (0)
 #define MOE_DECODE(D)                                                                         \
   case D:                                                                                     \
-    if (f8) {                                                                                 \
-      if (rt == 1) MOE_DECODE_RT(D, true, 1);                                                 \
-      else if (rt == 2) MOE_DECODE_RT(D, true, 2);                                            \
-      else MOE_DECODE_RT(D, true, 4);                                                         \
-    } else {                                                                                  \
-      if (rt == 1) MOE_DECODE_RT(D, false, 1);                                                \
-      else if (rt == 2) MOE_DECODE_RT(D, false, 2);                                           \
-      else MOE_DECODE_RT(D, false, 4);                                                        \
-    }                                                                                         \
+    if (f8) MOE_ROWS_F(D, true); else MOE_ROWS_F(D, false);                                   \
     break;
   switch (c.head_dim) {
     MOE_DECODE(64) MOE_DECODE(128) MOE_DECODE(256) MOE_DECODE(512)
     default: return hipErrorInvalidValue;
   }
 #undef MOE_DECODE
-#undef MOE_DECODE_RT
+#undef MOE_ROWS_F
+#undef MOE_ROWS
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t waves = (int64_t)c.batch * c.heads_kv * d.rows;
-  const dim3 jgrid((unsigned)((waves + 3) / 4));
+  const dim3 jgrid((unsigned)((int64_t)c.batch * c.heads_kv * d.rows));
 #define MOE_JOIN(D) \
   case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), jgrid, dim3(256), 0, st, a); break;
   switch (c.head_dim) { MOE_JOIN(64) MOE_JOIN(128) MOE_JOIN(256) MOE_JOIN(512) }

@@ -32,6 +32,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // 2^x by the hardware's exponential (about 1 ulp; 0 far below).
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Transposing LDS read: the 16 lanes of a quarter wave give the addresses of
+// 4 rows of 16 16-bit elements (lane i: row i / 4, elements 4 (i % 4) ..) and
+// lane i gets the 4 rows' element i.  Two of them are one bf16x8 operand of an MFMA.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ bf16x8 read_tr(const char* a, const char* b) {
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)b);
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// One asynchronous load of 16 bytes per lane from base + off into LDS at byte
+// `to` (wave-uniform) + 16 * lane.  In assembly because the compiler would
+// wait for it before the next LDS read, which never reads what it writes: the
+// kernels wait at the end of a step.  (m0 is this instruction's
+// alone: no other of the kernel's uses it.)
+__device__ __forceinline__ void load_lds16(uint32_t to, const char* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(to), "v"(off), "s"(base)
+               : "memory");
+}
+
+// Ends a step: every asynchronous load of this wave has landed and every wave
+// is done with the step's tiles.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The running maximum follows the scores only when one passes it by more than
+// this (base 2): weights then reach 2^kLag, which fp32 sums and bf16's
+// exponent hold as well, and the output is seldom rescaled.
+constexpr float kLag = 8.f;
+
 // Device check and cached properties (api.cpp).
 moe_status device_ok();
 

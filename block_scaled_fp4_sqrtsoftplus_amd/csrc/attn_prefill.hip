@@ -105,38 +105,12 @@ __device__ __forceinline__ int v_swz(int r) {
 }
 template <int D>
 __device__ __forceinline__ int k_at(int r, int c) {
-  return (r * (D / 8) + (c ^ k_swz<D>(r))) * 16;
+  return (r * (D / 8) + ((c & 15) ^ k_swz<D>(r))) * 16 + (c & ~15) * 16;
 }
 template <int D>
 __device__ __forceinline__ int v_at(int r, int c) {
-  return (r * (D / 8) + (c ^ v_swz<D>(r))) * 16;
+  return (r * (D / 8) + ((c & 15) ^ v_swz<D>(r))) * 16 + (c & ~15) * 16;
 }
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// One asynchronous load of 16 bytes per lane from base + off into LDS at byte
-// `to` (wave-uniform) + 16 * lane.  In assembly because the compiler would
-// wait for it before the next LDS read, which never reads what it writes: the
-// pipeline below waits at the end of the step.  (m0 is this instruction's
-// alone: no other of the kernel's uses it.)
-__device__ __forceinline__ void load_lds16(uint32_t to, const char* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"(to), "v"(off), "s"(base)
-               : "memory");
-}
-
-// Ends a step: every asynchronous load of this wave has landed and every wave
-// is done with the step's tiles.
-__device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// The running maximum follows the scores only when one passes it by more than
-// this (base 2): weights then reach 2^kLag, which fp32 sums and bf16's
-// exponent hold as well, and the output is seldom rescaled.
-constexpr float kLag = 8.f;
 
 // SPLIT waves share 32 rows (each has a D / SPLIT slice of both products'
 // columns, and they add their parts of S through LDS); 4 such groups make the
@@ -333,12 +307,8 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
             const int ch = 4 * (part * ND + d) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4*)(lds + (2 + buf) * TB + v_at<D>(r, ch) + half));
-            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4*)(lds + (2 + buf) * TB + v_at<D>(r + 8, ch) + half));
-            const bf16x8 vf = __builtin_bit_cast(
-                bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+            const char* vt = lds + (2 + buf) * TB + half;
+            const bf16x8 vf = read_tr(vt + v_at<D>(r, ch), vt + v_at<D>(r + 8, ch));
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
           }
         }

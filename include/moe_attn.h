@@ -67,7 +67,7 @@ typedef struct moe_kv_cache {
   int64_t pages;         /* >= 0 */
   int64_t stride_page;   /* elements (bf16: 2 bytes, FP8: 1 byte), of k and v alike; */
   int64_t stride_head;   /* multiples of 16 bytes, >= 0 */
-  int64_t stride_token;
+  int64_t stride_token;  /* at most 2^23 */
   int32_t page_size;     /* power of two in [16, 4096] */
   int32_t heads;         /* [1, 1024] */
   int32_t head_dim;      /* 64, 128, 256 or 512 */

@@ -60,7 +60,7 @@ def _append(cache=None, rope=None, tokens=3, slots=16, positions=16, k=None, v=N
     (SHAPE, dict(cache=_cache(page_size=8))), (SHAPE, dict(cache=_cache(heads=0))),
     (SHAPE, dict(cache=_cache(format=2))), (SHAPE, dict(cache=_cache(pages=-1))),
     (SHAPE, dict(cache=_cache(stride_page=-16))), (ALIGN, dict(cache=_cache(stride_token=132))),
-    (ALIGN, dict(cache=_cache(k=20))), (NULL, dict(cache=_cache(v=None))),
+    (SHAPE, dict(cache=_cache(stride_token=(1 << 23) + 16))), (ALIGN, dict(cache=_cache(k=20))), (NULL, dict(cache=_cache(v=None))),
     (NULL, dict(cache=_cache(format=1))), (ALIGN, dict(cache=_cache(format=1, k_scale=16, v_scale=17))),
     (ALIGN, dict(cache=_cache(format=1, k_scale=16, v_scale=16, stride_token=136))),
     (NULL, dict(k=_rows(p=None))), (ALIGN, dict(k=_rows(p=24))), (ALIGN, dict(v=_rows(stride_head=4))),
