@@ -519,7 +519,6 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   constexpr int WR = KT / 4;                  // rows per wave
   constexpr int RI = WR / LD;                 // rows per load of the wave
   static_assert(16 % WR == 0 && RI * LD == WR, "a wave's rows stay in one page");
-  const int sr = lane / C % (RI > 0 ? RI : 1), sc = lane % C;
   // page of the wave's rows, or -1: no key of them is read
   auto page_at = [&](int key0) {
     const int kt = (key0 + wave * WR) & ~15;
@@ -530,8 +529,10 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   u32x2 reg[FP8 ? NT : 1][FP8 ? LD : 1];      // FP8: codes of a step on their way
   uint32_t rsc[FP8 ? NT : 1][FP8 ? LD : 1];   // and their scale bytes
   // the chunk of its row that belongs at this lane's place of tile row tr
-  auto chunk = [&](int tr) { return (kv_at<D>(tr, sc) >> 4) - tr * C; };
+  auto chunk = [&](int tr, int c) { return (kv_at<D>(tr, c) >> 4) - tr * C; };
   auto fetch = [&](int buf, int key0) {
+    int sr = lane / C % RI, sc = lane % C;    // row among a load's, chunk of it
+    asm volatile("" : "+v"(sr), "+v"(sc));    // as below: no places kept over the loop
     const int pid = page_at(key0);
     const int kr = key0 + wave * WR;          // the wave's first key
     const int64_t off = (int64_t)max(pid, 0) * p.sp + h * p.sh + (int64_t)(kr & page_mask) * p.st;
@@ -546,7 +547,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
 #pragma unroll
         for (int i = 0; i < LD; ++i) {
           const int r = RI * i + sr;
-          const int c = chunk(wave * WR + r);
+          const int c = chunk(wave * WR + r, sc);
           reg[t][i] = u32x2{0, 0};
           rsc[t][i] = 127;
           if (r >= ra && r < rz) {
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
 #pragma unroll
         for (int i = 0; i < LD; ++i)
           load_lds16(to + RI * i * D * 2, base + RI * i * p.st,
-                     (uint32_t)(sr * (int)p.st + 16 * chunk(wave * WR + RI * i + sr)));
+                     (uint32_t)(sr * (int)p.st + 16 * chunk(wave * WR + RI * i + sr, sc)));
       }
     } else {
 #pragma unroll 1
@@ -573,7 +574,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
         u32x4 w = {0, 0, 0, 0};
         if (r >= ra && r < rz)
           w = *reinterpret_cast<const u32x4*>((t ? p.v : p.k) + off + r * p.st +
-                                              16 * chunk(wave * WR + r));
+                                              16 * chunk(wave * WR + r, sc));
         *reinterpret_cast<u32x4*>(lds + (2 * t + buf) * TB + (wave * WR + RI * i) * D * 2 +
                                   lane * 16) = w;
       }

@@ -224,6 +224,15 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
       fetch(0, buf ^ 1, key0 + BN);
       fetch(1, buf ^ 1, key0 + BN);
     }
+    // LDS places of this lane's first chunks: the swizzle is an exclusive or,
+    // so the other chunks' places are these with some bits flipped.  For large
+    // heads they are worked out anew in each step: kept over the loop they would
+    // take registers that it does not have (smaller ones are 5% faster with
+    // them kept).
+    int ka = buf * TB + k_at<D>(col, hh);
+    const int vr = 4 * hh + ((lane & 15) >> 2);
+    int va = (2 + buf) * TB + v_at<D>(vr, ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) + (lane & 1) * 8;
+    if constexpr (D >= 256) asm volatile("" : "+v"(ka), "+v"(va));
     f32x16 sc[NK];
     if (mine) {
 #pragma unroll
@@ -232,9 +241,11 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
         for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
+          // chunk 2 (part NF + j) + hh of row 32 t + col
+          const int c = 2 * j;
           const bf16x8 kf = __builtin_bit_cast(
-              bf16x8, *reinterpret_cast<const u32x4*>(lds + buf * TB +
-                                                      k_at<D>(32 * t + col, 2 * (part * NF + j) + hh)));
+              bf16x8, *reinterpret_cast<const u32x4*>(lds + (ka ^ ((c & 15) * 16)) + (c & ~15) * 16 +
+                                                      part * NF * 32 + 32 * t * D * 2));
           sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
         }
       }
@@ -302,13 +313,13 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
 #pragma unroll
           for (int i = 0; i < 4; ++i) pw[i] = pack_bf16(sc[t][8 * c + 2 * i], sc[t][8 * c + 2 * i + 1]);
           const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
-          const int r = 32 * t + 16 * c + 4 * hh + ((lane & 15) >> 2);
-          const int half = (lane & 1) * 8;
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
-            const int ch = 4 * (part * ND + d) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-            const char* vt = lds + (2 + buf) * TB + half;
-            const bf16x8 vf = read_tr(vt + v_at<D>(r, ch), vt + v_at<D>(r + 8, ch));
+            // chunks 4 (part ND + d) + .. of rows 32 t + 16 c + vr and 8 below
+            const int ch = 4 * d;
+            const char* v0 = lds + (va ^ ((ch & 15) * 16)) + (ch & ~15) * 16 + part * ND * 64 +
+                             (32 * t + 16 * c) * D * 2;
+            const bf16x8 vf = read_tr(v0, v0 + 8 * D * 2);
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
           }
         }
@@ -364,7 +375,7 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
   switch (c.head_dim) {
     MOE_PREFILL(64, 64, 1, 2)
     MOE_PREFILL(128, 64, 1, 2)
-    MOE_PREFILL(256, 32, 1, 1)
+    MOE_PREFILL(256, 32, 1, 2)
     MOE_PREFILL(512, 32, 2, 2)
     default: return hipErrorInvalidValue;
   }
