@@ -596,7 +596,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
 
   if (first < last) fetch(0, first);
   put(0);
-  step_barrier();
+  step_barrier<0>();
   int buf = 0;
   for (int key0 = first; key0 < last; key0 += KT, buf ^= 1) {
     const bool more = key0 + KT < last;
@@ -667,7 +667,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
       }
     }
     if (more) put(buf ^ 1);
-    step_barrier();
+    step_barrier<0>();
   }
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);

@@ -32,6 +32,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // 2^x by the hardware's exponential (about 1 ulp; 0 far below).
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The larger of a lane's and its partner's (lane ^ 32) value, in both.
+__device__ __forceinline__ float halves_max(float x) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // Transposing LDS read: the 16 lanes of a quarter wave give the addresses of
 // 4 rows of 16 16-bit elements (lane i: row i / 4, elements 4 (i % 4) ..) and
 // lane i gets the 4 rows' element i.  Two of them are one bf16x8 operand of an MFMA.
@@ -56,10 +62,11 @@ __device__ __forceinline__ void load_lds16(uint32_t to, const char* base, uint32
                : "memory");
 }
 
-// Ends a step: every asynchronous load of this wave has landed and every wave
-// is done with the step's tiles.
+// Ends a step: all but the last N of this wave's asynchronous loads have
+// landed, and every wave is done with the step's tiles.
+template <int N>
 __device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // The running maximum follows the scores only when one passes it by more than

@@ -19,6 +19,7 @@
 // few tokens: short prompts fill their tiles and little is computed above the
 // diagonal.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_internal.h"
 
@@ -112,21 +113,26 @@ __device__ __forceinline__ int v_at(int r, int c) {
   return (r * (D / 8) + ((c & 15) ^ v_swz<D>(r))) * 16 + (c & ~15) * 16;
 }
 
-// SPLIT waves share 32 rows (each has a D / SPLIT slice of both products'
-// columns, and they add their parts of S through LDS); 4 such groups make the
-// workgroup.  OCC: workgroups per CU the registers are held to, in waves per SIMD.
-template <int D, int BN, int SPLIT, int OCC>
-__global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillArgs p) {
-  constexpr int BM = 128;
-  constexpr int TH = 256 * SPLIT;
+// RG row groups of 32 rows; SPLIT waves share a group (each has a D / SPLIT
+// slice of both products' columns, and they add their parts of S through
+// LDS).  BN: keys per step.  BUFS: LDS tiles of K and of V, BUFS - 1 of them on
+// their way while one is read.  PIPE: a step takes the weights of its scores while the matrix
+// units take the next step's scores.  AHEAD: products by which LDS reads run
+// ahead of their use.  WAVES: waves per SIMD that the registers are held to.
+template <int D, int BN, int RG, int SPLIT, int BUFS, bool PIPE, int AHEAD, int WAVES>
+__global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(PrefillArgs p) {
+  constexpr int BM = 32 * RG;
+  constexpr int TH = 64 * RG * SPLIT;
   constexpr int NF = D / 16 / SPLIT;         // K fragments of a wave per 32 keys
   constexpr int ND = D / 32 / SPLIT;         // its column blocks of O
   constexpr int NK = BN / 32;                // 32-key tiles per step
   constexpr int C = D / 8;                   // 16-byte chunks per row
-  constexpr int LD = BN * C / TH;           // chunks a thread stages per tensor
+  constexpr int LD = BN * C / TH;            // chunks a thread stages per tensor
   constexpr int TB = BN * D * 2;             // bytes of one tile
-  constexpr int XB = SPLIT > 1 ? 4 * SPLIT * NK * 4096 : 0;   // the waves' parts of S
-  __shared__ __align__(16) char lds[4 * TB + XB];   // K, K, V, V, S
+  constexpr int V0 = BUFS * TB;              // the tiles of V
+  constexpr int X0 = 2 * BUFS * TB;          // the waves' parts of S
+  constexpr int XB = SPLIT > 1 ? RG * SPLIT * NK * 4096 : 0;
+  __shared__ __align__(16) char lds[X0 + XB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave = wv / SPLIT, part = wv % SPLIT;   // row group, slice of the columns
@@ -167,7 +173,6 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
   auto lo_of = [&](int t) { return p.window > 0 ? max(s.kn - s.qn + t + 1 - p.window, 0) : 0; };
   const int key_lo = lo_of(tok_a) / BN * BN, key_hi = hi_of(tok_z);
   const int all_lo = lo_of(wtok_z), all_hi = hi_of(wtok_a);   // kept by every row of the wave
-  const int any_lo = lo_of(wtok_a), any_hi = hi_of(wtok_z);   // kept by some row of it
 
   bf16x8 qf[NF];
   {
@@ -184,7 +189,7 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
   for (int d = 0; d < ND; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  float m = kNoMax, l = 0.f;
+  float m = kNoMax, l = 0.f, l2 = 0.f;   // two sums: shorter chains
 
   // Staging: chunk i of a thread is chunk tid + TH i of the tile, in row
   // r0 + RS i.  Its place in the row is permuted on the global side, since the
@@ -195,139 +200,298 @@ __global__ __launch_bounds__(256 * SPLIT, OCC) void attn_prefill_kernel(PrefillA
   const char* vb = reinterpret_cast<const char*>(p.v + s.k0 * p.v_st + h * p.v_sh);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int r0 = tid / C, c0 = tid % C;
+  // chunk i of a tile whose rows are all keys
+  auto fetch_one = [&](int which, int buf, int key0, int i) {
+    const int64_t st = 2 * (which ? p.v_st : p.k_st);
+    const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
+    load_lds16(lds0 + (which ? V0 : 0) + buf * TB + wv * 1024 + i * TH * 16,
+               (which ? vb : kb) + (key0 + RS * i) * st, (uint32_t)(r0 * (int)st + 16 * c));
+  };
   auto fetch = [&](int which, int buf, int key0) {   // which: 0 K, 1 V
     const char* base = which ? vb : kb;
     const int64_t st = 2 * (which ? p.v_st : p.k_st);
-    const uint32_t to = lds0 + (2 * which + buf) * TB + wv * 1024;
-    const bool whole = key0 + BN <= s.kn;
+    const uint32_t to = lds0 + (which ? V0 : 0) + buf * TB + wv * 1024;
+    if (key0 + BN <= s.kn) {
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
-      if (whole)
-        load_lds16(to + i * TH * 16, base + (key0 + RS * i) * st, (uint32_t)(r0 * (int)st + 16 * c));
-      else
+      for (int i = 0; i < LD; ++i) fetch_one(which, buf, key0, i);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < LD; ++i) {
+        const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
         load_lds16(to + i * TH * 16, base + key0 * st,
                    (uint32_t)(min(r0 + RS * i, s.kn - 1 - key0) * (int)st + 16 * c));
+      }
     }
   };
+  // LDS places of this lane's first chunks: the permutation is an exclusive or,
+  // so the other chunks' places are these with some bits flipped.  For large
+  // heads they are worked out anew in each step: kept over the loop they would
+  // take registers that it does not have.
+  const int k_lane = k_at<D>(col, hh);
+  const int v_lane = v_at<D>(4 * hh + ((lane & 15) >> 2), ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) +
+                     (lane & 1) * 8;
+  constexpr int QK = NK * NF, PV = 2 * NK * ND, NE = 16 * NK;
+  auto read_k = [&](int ka, int i) {   // operand of QK product i: tile i % NK, columns i / NK
+    const int t = i % NK, c = 2 * (i / NK);   // chunk 2 (part NF + ..) + hh of row 32 t + col
+    return __builtin_bit_cast(
+        bf16x8, *reinterpret_cast<const u32x4*>(lds + (ka ^ ((c & 15) * 16)) + (c & ~15) * 16 +
+                                                part * NF * 32 + 32 * t * D * 2));
+  };
+  auto read_v = [&](int va, int i) {   // operand of PV product i: keys i / ND, columns i % ND
+    const int ch = 4 * (i % ND);       // chunk 4 (part ND + ..) of rows 16 (i / ND) + .. and 8 below
+    const char* v0 = lds + (va ^ ((ch & 15) * 16)) + (ch & ~15) * 16 + part * ND * 64 +
+                     16 * (i / ND) * D * 2;
+    return read_tr(v0, v0 + 8 * D * 2);
+  };
+  float* xs = reinterpret_cast<float*>(lds + X0);
+  auto hand_over = [&](const f32x16(&sc)[NK]) {   // SPLIT 2: this wave's part for the other
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4*>(xs + ((wv * NK + t) * 4 + i / 4) * 256 + lane * 4) =
+            f32x4{sc[t][i], sc[t][i + 1], sc[t][i + 2], sc[t][i + 3]};
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
+  };
+  auto take_over = [&](f32x16(&sc)[NK]) {
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const f32x4 y =
+            *reinterpret_cast<const f32x4*>(xs + (((wv ^ 1) * NK + t) * 4 + i / 4) * 256 + lane * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][i + e] += y[e];
+      }
+  };
+  // whether every row of the wave keeps all of a step's keys; if not, the mask
+  auto inner = [&](int key0) { return key0 >= all_lo && key0 + BN <= all_hi; };
+  auto mask = [&](int key0, f32x16(&sc)[NK]) {
+    int first = key0 + 4 * hh;
+    asm volatile("" : "+v"(first));    // its places are not kept over the loop
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = first + 32 * t + 8 * (i >> 2) + (i & 3);
+        if (key >= row_hi || key < row_lo) sc[t][i] = -INFINITY;
+      }
+  };
+  auto largest = [&](const f32x16(&sc)[NK]) {
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 16 * NK; ++i)
+      x[i % 4] = i < 4 ? sc[i / 16][i % 16] : fmaxf(x[i % 4], sc[i / 16][i % 16]);
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  };
+  // takes the largest score of this lane's half of the row's keys
+  auto raise = [&](float mx) {
+    mx = halves_max(mx) * p.scale2;
+    if (__ballot(mx > m + kLag)) {
+      const float mn = fmaxf(m, mx);
+      const float a = exp2_fast(m - mn);
+      m = mn;
+      l *= a;
+      l2 *= a;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= a;
+    }
+  };
+
   const int steps = key_hi > key_lo ? (key_hi - key_lo + BN - 1) / BN : 0;
-  if (steps > 0) {
-    fetch(0, 0, key_lo);
-    fetch(1, 0, key_lo);
-  }
-  step_barrier();
-  for (int it = 0; it < steps; ++it) {
-    const int key0 = key_lo + it * BN;
-    const int buf = it & 1;
-    const bool mine = key0 < any_hi && key0 + BN > any_lo;   // wave-uniform
-    if (it + 1 < steps) {
-      fetch(0, buf ^ 1, key0 + BN);
-      fetch(1, buf ^ 1, key0 + BN);
+  u32x4 pw[2 * NK];
+  // the weight of element e of the step, in three parts that may be apart
+  auto weight_arg = [&](f32x16(&sc)[NK], int e) {
+    sc[e / 16][e % 16] = fmaf(sc[e / 16][e % 16], p.scale2, -m);
+  };
+  auto weight_exp = [&](f32x16(&sc)[NK], int e) {
+    sc[e / 16][e % 16] = exp2_fast(sc[e / 16][e % 16]);
+  };
+  auto weight_sum = [&](const f32x16(&sc)[NK], int e) {
+    const float w = sc[e / 16][e % 16];
+    if (e & 1) {
+      l2 += w;
+      pw[e / 8][e / 2 % 4] = pack_bf16(sc[e / 16][e % 16 - 1], w);
+    } else {
+      l += w;
     }
-    // LDS places of this lane's first chunks: the swizzle is an exclusive or,
-    // so the other chunks' places are these with some bits flipped.  For large
-    // heads they are worked out anew in each step: kept over the loop they would
-    // take registers that it does not have (smaller ones are 5% faster with
-    // them kept).
-    int ka = buf * TB + k_at<D>(col, hh);
-    const int vr = 4 * hh + ((lane & 15) >> 2);
-    int va = (2 + buf) * TB + v_at<D>(vr, ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) + (lane & 1) * 8;
-    if constexpr (D >= 256) asm volatile("" : "+v"(ka), "+v"(va));
-    f32x16 sc[NK];
-    if (mine) {
+  };
+  auto weight = [&](f32x16(&sc)[NK], int e) {
+    weight_arg(sc, e);
+    weight_exp(sc, e);
+    weight_sum(sc, e);
+  };
+  auto scores = [&](int buf, f32x16(&to)[NK]) {
+    int ka = buf * TB + k_lane;
+    if constexpr (D >= 256) asm volatile("" : "+v"(ka));
 #pragma unroll
-      for (int t = 0; t < NK; ++t) {
+    for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+      for (int i = 0; i < 16; ++i) to[t][i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) {
-          // chunk 2 (part NF + j) + hh of row 32 t + col
-          const int c = 2 * j;
-          const bf16x8 kf = __builtin_bit_cast(
-              bf16x8, *reinterpret_cast<const u32x4*>(lds + (ka ^ ((c & 15) * 16)) + (c & ~15) * 16 +
-                                                      part * NF * 32 + 32 * t * D * 2));
-          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], sc[t], 0, 0, 0);
-        }
+    for (int i = 0; i < QK; ++i)
+      to[i % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(ka, i), qf[i / NK], to[i % NK], 0, 0, 0);
+  };
+  auto values = [&](int buf) {
+    int va = V0 + buf * TB + v_lane;
+    if constexpr (D >= 256) asm volatile("" : "+v"(va));
+#pragma unroll
+    for (int i = 0; i < PV; ++i)
+      o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          read_v(va, i), __builtin_bit_cast(bf16x8, pw[i / ND]), o[i % ND], 0, 0, 0);
+  };
+  if constexpr (PIPE) {
+    // K runs one step ahead of V.  At step it, K of it + 1 and V of it are in
+    // LDS, K up to it + BUFS - 1 and V up to it + BUFS - 2 on their way.
+    f32x16 sc[NK], nx[NK];
+    if (steps > 0) {
+#pragma unroll
+      for (int i = 0; i < BUFS; ++i) {
+        if (i < steps) fetch(0, i, key_lo + i * BN);
+        if (i < BUFS - 1 && i < steps) fetch(1, i, key_lo + i * BN);
       }
+      step_barrier<0>();
+      scores(0, sc);
+      if constexpr (SPLIT == 2) {
+        hand_over(sc);
+        take_over(sc);
+      }
+      if (!inner(key_lo)) mask(key_lo, sc);
+      raise(largest(sc));
+      step_barrier<0>();
     }
-    if constexpr (SPLIT == 2) {
-      float* x = reinterpret_cast<float*>(lds + 4 * TB);
-      if (mine) {
-#pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<f32x4*>(x + ((wv * NK + t) * 4 + i / 4) * 256 + lane * 4) =
-                f32x4{sc[t][i], sc[t][i + 1], sc[t][i + 2], sc[t][i + 3]};
+    int kb_next = 1 % BUFS, vb_now = 0;      // tiles of K of it + 1, V of it
+    // WHOLE: every row of the tiles it asks for is a key's, and the next step's scores
+    // need no mask.  Then the loads are dealt out behind the QK products (a
+    // wave that issues them at once waits for the address unit, which takes
+    // them one by one) and the next maximum behind the PV products.
+    auto step = [&](int it, f32x16(&sc)[NK], f32x16(&nx)[NK], auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      const int key0 = key_lo + it * BN;
+      const int vb_free = vb_now == 0 ? BUFS - 1 : vb_now - 1;
+      const int kb_free = kb_next == 0 ? BUFS - 1 : kb_next - 1;
+      if constexpr (!WHOLE) {
+        if (it + BUFS < steps) fetch(0, kb_free, key0 + BUFS * BN);
+        if (it + BUFS - 1 < steps) fetch(1, vb_free, key0 + (BUFS - 1) * BN);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
-      if (mine) {
-#pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const f32x4 y = *reinterpret_cast<const f32x4*>(
-                x + (((wv ^ 1) * NK + t) * 4 + i / 4) * 256 + lane * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[t][i + e] += y[e];
-          }
-      }
-    }
-    if (mine) {
-      if (!(key0 >= all_lo && key0 + BN <= all_hi)) {
-#pragma unroll
-        for (int t = 0; t < NK; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = key0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3);
-            if (key >= row_hi || key < row_lo) sc[t][i] = -INFINITY;
-          }
-      }
-      float mx = sc[0][0];
+      // One stream of matrix instructions in an order fixed by hand: the QK
+      // products of the next step, the weights of this one dealt out
+      // behind them, then the PV products.
+      int ka = kb_next * TB + k_lane, va = V0 + vb_now * TB + v_lane;
+      asm volatile("" : "+v"(ka), "+v"(va));
+      auto read = [&](int i) { return i < QK ? read_k(ka, i) : read_v(va, i - QK); };
+      constexpr int PER = NE / QK;
+      static_assert(PER * QK == NE, "");
 #pragma unroll
       for (int t = 0; t < NK; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[t][i]);
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      mx *= p.scale2;
-      if (__ballot(mx > m + kLag)) {
-        const float mn = fmaxf(m, mx);
-        const float a = exp2_fast(m - mn);
-        m = mn;
-        l *= a;
+        for (int i = 0; i < 16; ++i) nx[t][i] = 0.f;
+      bf16x8 f[AHEAD];
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+      for (int i = 0; i < AHEAD; ++i) f[i] = read(i);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][i] *= a;
-      }
+      for (int i = 0; i < QK; ++i) {
+        nx[i % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD], qf[i / NK], nx[i % NK], 0, 0, 0);
+        f[i % AHEAD] = read(i + AHEAD);
 #pragma unroll
-      for (int t = 0; t < NK; ++t) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          sc[t][i] = exp2_fast(fmaf(sc[t][i], p.scale2, -m));
-          l += sc[t][i];
+        for (int e = 0; e < PER; ++e) {      // three products' elements at once: no part waits
+          if (i >= 2) weight_sum(sc, (i - 2) * PER + e);
+          if (i >= 1) weight_exp(sc, (i - 1) * PER + e);
+          weight_arg(sc, i * PER + e);
         }
+        if constexpr (WHOLE) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          u32x4 pw;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pw[i] = pack_bf16(sc[t][8 * c + 2 * i], sc[t][8 * c + 2 * i + 1]);
-          const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            // chunks 4 (part ND + d) + .. of rows 32 t + 16 c + vr and 8 below
-            const int ch = 4 * d;
-            const char* v0 = lds + (va ^ ((ch & 15) * 16)) + (ch & ~15) * 16 + part * ND * 64 +
-                             (32 * t + 16 * c) * D * 2;
-            const bf16x8 vf = read_tr(v0, v0 + 8 * D * 2);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf, o[d], 0, 0, 0);
+          for (int j = i * 2 * LD / QK; j < (i + 1) * 2 * LD / QK; ++j) {
+            if (j < LD) fetch_one(0, kb_free, key0 + BUFS * BN, j);
+            else fetch_one(1, vb_free, key0 + (BUFS - 1) * BN, j - LD);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int e = (QK - 1) * PER; e < NE; ++e) weight_exp(sc, e);
+      if constexpr (SPLIT == 2) hand_over(nx);
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < PV; ++i) {
+        o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            f[(QK + i) % AHEAD], __builtin_bit_cast(bf16x8, pw[i / ND]), o[i % ND], 0, 0, 0);
+        if (i + AHEAD < PV) f[(QK + i) % AHEAD] = read(QK + i + AHEAD);
+        if (i < 2) {                         // the last two products' weights
+#pragma unroll
+          for (int e = 0; e < PER; ++e) weight_sum(sc, (QK - 2 + i) * PER + e);
+        }
+        if constexpr (WHOLE && SPLIT == 1) {
+#pragma unroll
+          for (int e = i * NE / PV; e < (i + 1) * NE / PV; ++e)
+            mx[e % 4] = e < 4 ? nx[e / 16][e % 16] : fmaxf(mx[e % 4], nx[e / 16][e % 16]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (SPLIT == 2) take_over(nx);
+      if constexpr (WHOLE && SPLIT == 1) {
+        raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      } else {
+        if (!WHOLE && !inner(key0 + BN)) mask(key0 + BN, nx);
+        raise(largest(nx));
+      }
+      kb_next = kb_next + 1 == BUFS ? 0 : kb_next + 1;
+      vb_now = vb_now + 1 == BUFS ? 0 : vb_now + 1;
+      // what this step has asked for may stay on its way
+      if constexpr (WHOLE) step_barrier<(BUFS - 2) * 2 * LD>(); else step_barrier<0>();
+    };
+    auto whole = [&](int it) {
+      return it + BUFS < steps && key_lo + (it + BUFS + 1) * BN <= s.kn && inner(key_lo + (it + 1) * BN);
+    };
+    int it = 0;
+    while (it + 1 < steps) {
+      for (; whole(it) && whole(it + 1); it += 2) {   // two at a time: scores change places
+        step(it, sc, nx, std::true_type{});
+        step(it + 1, nx, sc, std::true_type{});
+      }
+      if (it + 1 < steps) {
+        step(it, sc, nx, std::false_type{});
+#pragma unroll
+        for (int t = 0; t < NK; ++t) sc[t] = nx[t];
+        ++it;
       }
     }
-    step_barrier();
+    if (steps > 0) {
+#pragma unroll
+      for (int e = 0; e < NE; ++e) weight(sc, e);
+      values(vb_now);
+    }
+  } else {
+    if (steps > 0) {
+      fetch(0, 0, key_lo);
+      fetch(1, 0, key_lo);
+    }
+    step_barrier<0>();
+    for (int it = 0; it < steps; ++it) {
+      const int key0 = key_lo + it * BN;
+      const int buf = it & 1;
+      if (it + 1 < steps) {
+        fetch(0, buf ^ 1, key0 + BN);
+        fetch(1, buf ^ 1, key0 + BN);
+      }
+      f32x16 sc[NK];
+      scores(buf, sc);
+      if constexpr (SPLIT == 2) {
+        hand_over(sc);
+        take_over(sc);
+      }
+      if (!inner(key0)) mask(key0, sc);
+      raise(largest(sc));
+#pragma unroll
+      for (int e = 0; e < NE; ++e) weight(sc, e);
+      values(buf);
+      step_barrier<0>();
+    }
   }
 
+  l += l2;
   l += __shfl_xor(l, 32);
   if (!live) return;
   const float inv = l > 0.f ? 1.0f / l : 0.f;
@@ -363,20 +527,19 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
   a.causal = c.causal; a.window = c.window;
   a.q_flip = c.scale < 0.f ? 0x80008000u : 0u;
   a.scale2 = (c.scale < 0.f ? -c.scale : c.scale) * kLog2e;
-  // at most one partly filled tile per sequence
-  const int64_t tiles =
-      c.tokens * a.group / 128 + std::min<int64_t>(c.batch, c.tokens);
-  const dim3 grid((unsigned)(tiles * c.heads_kv));
-#define MOE_PREFILL(D, BN, SPLIT, OCC)                                                        \
-  case D:                                                                                     \
-    hipLaunchKernelGGL((attn_prefill_kernel<D, BN, SPLIT, OCC>), grid, dim3(256 * SPLIT), 0, st, \
-                       a);                                                                    \
-    break;
+#define MOE_PREFILL(D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES)                               \
+  case D: {                                                                                   \
+    /* at most one partly filled tile per sequence */                                         \
+    const int64_t tiles = c.tokens * a.group / (32 * RG) + std::min<int64_t>(c.batch, c.tokens); \
+    hipLaunchKernelGGL((attn_prefill_kernel<D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES>),            \
+                       dim3((unsigned)(tiles * c.heads_kv)), dim3(64 * RG * SPLIT), 0, st, a); \
+    break;                                                                                    \
+  }
   switch (c.head_dim) {
-    MOE_PREFILL(64, 64, 1, 2)
-    MOE_PREFILL(128, 64, 1, 2)
-    MOE_PREFILL(256, 32, 1, 2)
-    MOE_PREFILL(512, 32, 2, 2)
+    MOE_PREFILL(64, 64, 4, 1, 2, false, 4, 2)
+    MOE_PREFILL(128, 64, 4, 1, 2, true, 3, 2)
+    MOE_PREFILL(256, 32, 4, 1, 3, true, 2, 2)
+    MOE_PREFILL(512, 32, 4, 2, 2, false, 2, 2)
     default: return hipErrorInvalidValue;
   }
 #undef MOE_PREFILL
