@@ -127,7 +127,9 @@ moe_status moe_attn_decode(const moe_attn_config* cfg, const moe_rows* q,
   if (s != MOE_OK) return s;
   if ((s = check_cache(cache)) != MOE_OK) return s;
   if (cache->heads != cfg->heads_kv || cache->head_dim != cfg->head_dim) return MOE_ERR_BAD_SHAPE;
-  if (table_width < 0 || (int64_t)table_width * cache->page_size > (int64_t(1) << 30))
+  const int64_t longest = (int64_t)table_width * cache->page_size;
+  if (table_width < 0 || longest > (int64_t(1) << 30) ||
+      cfg->batch * (longest / 64 + 1) >= (int64_t(1) << 31))   // tiles are counted in 32 bits
     return MOE_ERR_BAD_SHAPE;
   const bool used = cfg->batch > 0;
   if ((s = check_rows(q, used)) != MOE_OK) return s;

@@ -28,10 +28,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kTileKeys = 128;     // unit of the split over a sequence's keys
 // Workgroups the tiles are dealt to, by the kernel that takes them.
-constexpr int kSplitTarget = 1024;
-constexpr int kSplitTargetRows = 256;
+constexpr int kPieces = 512;
+constexpr int kPiecesRows = 256;
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -50,10 +49,10 @@ struct DecodeArgs {
   int batch, q_len, hq, hkv, group, rows, rgroups;
   int window;
   float scale2;            // scale * log2(e)
-  int target;              // splits over all sequences, for one head and row group
-  int slots;               // grid bound: target + batch
-  float* part_o;           // [slots][hkv][rows][D]
-  float* part_m;           // [slots][hkv][rows] maximum (base 2)
+  int pieces;              // the work's, for one head and row group
+  int tile_shift;          // keys per tile, the unit of the cut: 2^tile_shift
+  float* part_o;           // [pieces + batch][hkv][rows][D]
+  float* part_m;           // [pieces + batch][hkv][rows] maximum (base 2)
   float* part_l;           // ... and sum
   int2* meta;              // [batch] first slot, splits
 };
@@ -63,8 +62,7 @@ __device__ __forceinline__ int entry(const int32_t* t, int64_t i) {
   return *(const __attribute__((address_space(4))) int32_t*)(t + i);
 }
 
-// Keys a sequence's rows may reach: [lo, len), and how many 128-key tiles
-// that is, counted from lo rounded down to a step of 32.
+// Keys a sequence's rows may reach: [lo, len), and how many tiles that is, counted from lo rounded down to a step of 32 (1 for none).
 struct Range {
   int lo, len, tiles;
 };
@@ -79,56 +77,114 @@ __device__ __forceinline__ Range range_of(const DecodeArgs& p, int raw_len) {
     r.lo = (int)max(lo, (int64_t)0);
   }
   const int span = r.len - (r.lo & ~31);
-  r.tiles = r.len > r.lo ? (span + kTileKeys - 1) / kTileKeys : 0;
+  r.tiles = r.len > r.lo ? (span + (1 << p.tile_shift) - 1) >> p.tile_shift : 1;
   return r;
 }
 
-// Which sequence and split a slot is: tiles are dealt c to a split, c the
-// ceiling of all tiles over `target`; a sequence has at least one split, so
-// that an empty one still has its rows written.  Every wave works it out for
-// itself, 64 sequences at a time.
+// The work of all sequences, laid end to end in tiles, is cut into pieces of
+// equal length, one per workgroup (of a head and row group); a piece covers
+// the end of a sequence, whole ones and the start of another.  An empty sequence
+// counts a tile, so that a piece writes its rows.  Sequence b's part of piece w
+// is a split with slot w + b: every step along the work raises one of the two,
+// so slots differ, and those of a sequence are consecutive.
 struct Piece {
-  int b, split, splits, slot0, c;
+  int w;            // piece
+  uint32_t per;     // tiles per piece
+  uint32_t at, end; // first tile, and past the last one
+  int b, tile, len; // the sequence of the first one, the tile's place there, seq_lens[b]
 };
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) x += __shfl_xor(x, off);
-  return x;
-}
-__device__ __forceinline__ bool find_piece(const DecodeArgs& p, int slot, Piece& out) {
+// Every wave works its piece out for itself, 64 sequences at a time.
+__device__ __forceinline__ bool find_piece(const DecodeArgs& p, int w, Piece& out) {
   const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  int mine = 0;   // tiles of the last 64 sequences looked at
+  uint32_t total = 0;   // the host has checked that it stays below 2^31
+  int raw = 0, mine = 0, incl = 0;   // the last 64 sequences looked at
+  auto look = [&](int b0) {
+    raw = b0 + lane < p.batch ? p.seq_lens[b0 + lane] : 0;
+    mine = b0 + lane < p.batch ? range_of(p, raw).tiles : 0;
+    incl = wave_scan(mine);
+  };
   for (int b0 = 0; b0 < p.batch; b0 += 64) {
-    mine = b0 + lane < p.batch ? range_of(p, p.seq_lens[b0 + lane]).tiles : 0;
-    total += wave_sum(mine);
+    look(b0);
+    total += __builtin_amdgcn_readlane(incl, 63);
   }
-  const int c = (int)max((total + p.target - 1) / p.target, (int64_t)1);
-  int base = 0;
+  out.w = w;
+  out.per = (total + p.pieces - 1) / p.pieces;
+  out.at = (uint32_t)min((uint64_t)w * out.per, (uint64_t)total);
+  out.end = min(out.at + out.per, total);
+  if (out.at >= total) return false;
+  uint32_t base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 64) {
-    if (p.batch > 64)
-      mine = b0 + lane < p.batch ? range_of(p, p.seq_lens[b0 + lane]).tiles : 0;
-    const int n = b0 + lane < p.batch ? max((mine + c - 1) / c, 1) : 0;
-    int incl = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
-    const uint64_t past = __ballot(base + incl > slot);
+    if (p.batch > 64) look(b0);
+    const uint64_t past = __ballot(base + incl > out.at);
     if (past) {
       const int l = __builtin_ctzll(past);
       out.b = __builtin_amdgcn_readfirstlane(b0 + l);
-      out.splits = __builtin_amdgcn_readlane(n, l);
-      out.slot0 = base + __builtin_amdgcn_readlane(incl, l) - out.splits;
-      out.split = slot - out.slot0;
-      out.c = __builtin_amdgcn_readfirstlane(c);
+      out.len = __builtin_amdgcn_readlane(raw, l);
+      out.tile = (int)(out.at - base) -
+                 (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(mine, l));
       return true;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
+
+// One sequence's part of a piece.
+struct Part {
+  int b, slot, splits;
+  bool starts;      // holds the sequence's first tile
+  Range rng;
+  int first, last;  // keys
+};
+__device__ __forceinline__ Part part_of(const DecodeArgs& p, const Piece& pc) {
+  Part x;
+  x.b = pc.b;
+  x.slot = pc.w + pc.b;
+  x.rng = range_of(p, pc.len);
+  const uint32_t begin = pc.at - pc.tile;   // the sequence's first tile in all the work
+  x.splits = (int)((begin + x.rng.tiles - 1) / pc.per - begin / pc.per) + 1;
+  x.starts = pc.tile == 0;
+  const int n = min((int)(pc.end - pc.at), x.rng.tiles - pc.tile);
+  x.first = (x.rng.lo & ~31) + (pc.tile << p.tile_shift);
+  x.last = (int)min((int64_t)x.rng.len, (int64_t)x.first + ((int64_t)n << p.tile_shift));
+  return x;
+}
+__device__ __forceinline__ void advance(const DecodeArgs& p, const Part& x, Piece& pc) {
+  pc.at += x.rng.tiles - pc.tile;          // past the end where the part is the piece's last
+  pc.tile = 0;
+  ++pc.b;
+  if (pc.at < pc.end) pc.len = entry(p.seq_lens, pc.b);
+}
+
+// Pages of 64 consecutive 16-key tiles, one per lane (-1: no key of the tile is
+// read), with the next 64 on their way: a step gets its page from a lane instead
+// of waiting for a load.
+struct Pages {
+  const int32_t* row;
+  int len, lo, base, now, next;
+  __device__ __forceinline__ int load(const DecodeArgs& p, int tile) const {
+    const int64_t key = 16 * ((int64_t)tile + (threadIdx.x & 63));
+    if (!(key < len && key + 16 > lo)) return -1;
+    const int id = row[key >> p.page_shift];
+    return id >= 0 && id < p.pages ? id : -1;
+  }
+  __device__ __forceinline__ Pages(const DecodeArgs& p, const Part& pt)
+      : row(p.table + (int64_t)pt.b * p.table_width), len(pt.rng.len), lo(pt.rng.lo),
+        base(pt.first >> 4) {
+    now = load(p, base);
+    next = load(p, base + 64);
+  }
+  // the page of the tile that key begins or lies in; keys do not go back past a window
+  __device__ __forceinline__ int at(const DecodeArgs& p, int key) {
+    const int t = key >> 4;
+    if (t >= base + 64) {
+      base += 64;
+      now = next;
+      next = load(p, base + 64);
+    }
+    return __builtin_amdgcn_readlane(now, t - base);
+  }
+};
 
 __device__ __forceinline__ float scale_of(uint32_t byte) {   // 2^(byte - 127)
   return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
@@ -179,11 +235,11 @@ __device__ __forceinline__ void join_waves(float* lds, int kp, int rt, float& m,
 // else the split's partial result.  A lane has NQ quads of its row: columns
 // col(i) .. + 3, values val(i).
 template <int D, int NQ, class Col, class Val>
-__device__ __forceinline__ void finish(const DecodeArgs& p, const Piece& pc, int slot, int h, int rg,
+__device__ __forceinline__ void finish(const DecodeArgs& p, const Part& pc, int h, int rg,
                                        int row, bool row_live, int64_t qrow, int head, int g,
                                        float m, float l, Col col, Val val) {
-  if (pc.split == 0 && h == 0 && rg == 0 && threadIdx.x == 0)
-    p.meta[pc.b] = make_int2(pc.slot0, pc.splits);
+  if (pc.starts && h == 0 && rg == 0 && threadIdx.x == 0)
+    p.meta[pc.b] = make_int2(pc.slot, pc.splits);
   if (!row_live) return;
   if (pc.splits == 1) {
     const float inv = l > 0.f ? 1.0f / l : 0.f;
@@ -196,7 +252,7 @@ __device__ __forceinline__ void finish(const DecodeArgs& p, const Piece& pc, int
     if (p.lse && g == 0)
       p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
   } else {
-    const int64_t idx = ((int64_t)slot * p.hkv + h) * p.rows + row;
+    const int64_t idx = ((int64_t)pc.slot * p.hkv + h) * p.rows + row;
     float* dst = p.part_o + idx * D;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) *reinterpret_cast<f32x4*>(dst + col(i)) = val(i);
@@ -210,7 +266,7 @@ __device__ __forceinline__ void finish(const DecodeArgs& p, const Piece& pc, int
 // Up to 16 rows for a key-value head: each of 4 waves takes every fourth step of 32 keys,
 // from memory to registers.
 template <int D, bool FP8>
-__global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
+__global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
   constexpr int KP = 4;
   constexpr int NF = D / 32;                  // K fragments per 16-key tile
   constexpr int DV = D < 128 ? D / 16 : 8;    // columns of V per lane and block
@@ -218,27 +274,28 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
   constexpr int NG = D < 128 ? 1 : D / 128;   // FP8 scales per row
   constexpr int EB = FP8 ? 1 : 2;             // bytes per element
   constexpr int VW = DV * EB / 4;             // dwords of V per lane, row and block
+  constexpr int NL = FP8 ? NF / 2 : NF;       // 16-byte loads of K per lane and tile
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int kp = wave;
 
-  const int slot = blockIdx.x / p.hkv;
-  const int h = blockIdx.x - slot * p.hkv;
+  const int piece = blockIdx.x / p.hkv;
+  const int h = blockIdx.x - piece * p.hkv;
   constexpr int rg = 0;
   Piece pc;
-  if (!find_piece(p, slot, pc)) return;
-  const Range rng = range_of(p, entry(p.seq_lens, pc.b));
-  const int len = rng.len, lo = rng.lo;
-  const int first = (lo & ~31) + pc.split * pc.c * kTileKeys;
-  const int last = (int)min((int64_t)len, (int64_t)first + (int64_t)pc.c * kTileKeys);
+  if (!find_piece(p, piece, pc)) return;
+  while (pc.at < pc.end) {
+  const Part pt = part_of(p, pc);
+  advance(p, pt, pc);
+  const int len = pt.rng.len, lo = pt.rng.lo, first = pt.first, last = pt.last;
 
   // this lane's row: token, head and the keys it keeps [row_lo, row_hi)
   const int row = col;
   const bool row_live = row < p.rows;
   const int tok = row_live ? row / p.group : 0;
   const int head = row_live ? h * p.group + row - tok * p.group : 0;
-  const int64_t qrow = (int64_t)pc.b * p.q_len + tok;
+  const int64_t qrow = (int64_t)pt.b * p.q_len + tok;
   const int row_hi = len - p.q_len + 1 + tok;
   const int row_lo = p.window > 0 ? row_hi - p.window : 0;
   // every row keeps the keys of [all_lo, all_hi)
@@ -262,7 +319,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
     for (int i = 0; i < DV; ++i) o[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = kNoMax, l = 0.f;
 
-  const int32_t* trow = p.table + (int64_t)pc.b * p.table_width;
+  Pages pages(p, pt);
   const char* kh = p.k + h * p.sh;
   const char* vh = p.v + h * p.sh;
   const int page_mask = (1 << p.page_shift) - 1;
@@ -273,10 +330,9 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int kt = key0 + 16 * t;
-      have[t] = kt < len && kt + 16 > lo;
-      int pid = have[t] ? entry(trow, kt >> p.page_shift) : 0;
-      have[t] = have[t] && pid >= 0 && pid < p.pages;
-      pid = have[t] ? pid : 0;
+      int pid = pages.at(p, kt);
+      have[t] = pid >= 0;
+      pid = max(pid, 0);
       off[t] = pid * p.sp + (int64_t)(kt & page_mask) * p.st;
       srow[t] = (((int64_t)pid * p.hkv + h) << p.page_shift) + (kt & page_mask);
     }
@@ -284,14 +340,22 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
 
     // K, 16 keys a tile, and V
     f32x4 s[2];
-    u32x4 kr[2][FP8 ? NF / 2 : NF];
+    u32x4 kr[2][NL];
     uint32_t ksc[2][NG];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const char* kb = kh + off[t] + col * p.st;
+      if constexpr (D * EB >= 128) {
+        // whole 128-byte lines of 8 rows a load, then into operand order
+        const char* kb = kh + off[t] + (col & 7) * p.st + 64 * (col >> 3) + 16 * g;
 #pragma unroll
-      for (int j = 0; j < (FP8 ? NF / 2 : NF); ++j)
-        kr[t][j] = *reinterpret_cast<const u32x4*>(kb + 64 * j + 16 * g);
+        for (int j = 0; j < NL; j += 2) {
+          kr[t][j] = wload<u32x4>(kb + 64 * j);
+          kr[t][j + 1] = wload<u32x4>(kb + 64 * j + 8 * p.st);
+        }
+      } else {
+        const char* kb = kh + off[t] + col * p.st;
+        kr[t][0] = *reinterpret_cast<const u32x4*>(kb + 16 * g);
+      }
       if constexpr (FP8) {
 #pragma unroll
         for (int n = 0; n < NG; ++n) ksc[t][n] = p.ks[(srow[t] + col) * NG + n];
@@ -307,11 +371,11 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           if constexpr (VW == 4) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(vb + b * 16 * DV * EB);
+            const u32x4 w = wload<u32x4>(vb + b * 16 * DV * EB);
 #pragma unroll
             for (int i = 0; i < 4; ++i) vr[4 * t + r][b][i] = w[i];
           } else if constexpr (VW == 2) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(vb + b * 16 * DV * EB);
+            const u32x2 w = wload<u32x2>(vb + b * 16 * DV * EB);
             vr[4 * t + r][b][0] = w[0];
             vr[4 * t + r][b][1] = w[1];
           } else {
@@ -328,6 +392,9 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (D * EB >= 128)
+#pragma unroll
+        for (int j = 0; j < NL; j += 2) line_pair_to_steps(kr[t][j], kr[t][j + 1]);
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
         bf16x8 kf;
@@ -375,8 +442,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) mx = fmaxf(mx, pr[i]);
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = quarters_max(mx);
     if (__ballot(mx > m + kLag)) {
       const float mn = fmaxf(m, mx);
       const float a = exp2_fast(m - mn);
@@ -430,17 +496,18 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(DecodeArgs p) {
 
   __shared__ float lds[KP / 2 * (NB * DV * 256 + 128)];
   join_waves<KP, 1, NB * DV>(lds, kp, 0, m, l, &o[0][0]);
-  if (kp > 0) return;
+  if (kp > 0) continue;
 
   // quad i: block b, row r of V's operand, columns 4 c of the lane's DV
   constexpr int QD = DV / 4;
   finish<D, NB * 4 * QD>(
-      p, pc, slot, h, rg, row, row_live, qrow, head, g, m, l,
+      p, pt, h, rg, row, row_live, qrow, head, g, m, l,
       [&](int i) { return i / (4 * QD) * 16 * DV + (4 * g + i / QD % 4) * DV + i % QD * 4; },
       [&](int i) {
         const int b = i / (4 * QD), r = i / QD % 4, c = i % QD * 4;
         return f32x4{o[b][c][r], o[b][c + 1][r], o[b][c + 2][r], o[b][c + 3][r]};
       });
+  }
 }
 
 // Position of 16-byte chunk c of row r in an LDS tile whose rows serve as keys
@@ -454,14 +521,13 @@ __device__ __forceinline__ int kv_at(int r, int c) {
 }
 
 // More than 16 rows for a key-value head: RT row tiles of 16 (2 or 4), one per
-// wave, share K and V through LDS, and 4 / RT waves share a row tile, 32 keys
-// of a step each.  A step's tiles are loaded while the one before is computed:
+// wave, share K and V through LDS, and KP waves share a row tile, 32 keys of a
+// step each.  A step's tiles are loaded while the one before is computed:
 // bf16 straight into LDS, FP8 through registers, turned into bf16 once for all waves.
 // ONE: one tensor serves as keys and values, and is loaded once.
-template <int D, bool FP8, int RT, bool ONE>
-__global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_rows_kernel(
+template <int D, bool FP8, int RT, int KP, bool ONE>
+__global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_decode_rows_kernel(
     DecodeArgs p) {
-  constexpr int KP = 4 / RT;
   constexpr int KT = 32 * KP;                 // keys per step
   constexpr int NF = D / 32;
   constexpr int NB = D / 16;
@@ -469,7 +535,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   constexpr int NG = D < 128 ? 1 : D / 128;
   constexpr int TB = KT * D * 2;
   constexpr int NT = ONE ? 1 : 2;
-  constexpr int LD = KT * C / 256;            // chunks a thread stages per tensor
+  constexpr int LD = C / (2 * RT);            // chunks a thread stages per tensor
   constexpr int JOIN = KP > 1 ? RT * (KP / 2) * (NB * 256 + 128) * 4 : 0;
   constexpr int LDS = 2 * NT * TB > JOIN ? 2 * NT * TB : JOIN;
   __shared__ __align__(16) char lds[LDS];
@@ -478,22 +544,23 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   const int col = lane & 15, g = lane >> 4;
   const int rt = wave % RT, kp = wave / RT;
 
-  const int per_slot = p.hkv * p.rgroups;
-  const int slot = blockIdx.x / per_slot;
-  const int rest = blockIdx.x - slot * per_slot;
+  const int per_piece = p.hkv * p.rgroups;
+  const int piece = blockIdx.x / per_piece;
+  const int rest = blockIdx.x - piece * per_piece;
   const int rg = rest / p.hkv, h = rest - rg * p.hkv;
   Piece pc;
-  if (!find_piece(p, slot, pc)) return;
-  const Range rng = range_of(p, entry(p.seq_lens, pc.b));
-  const int len = rng.len, lo = rng.lo;
-  const int first = (lo & ~31) + pc.split * pc.c * kTileKeys;
-  const int last = (int)min((int64_t)len, (int64_t)first + (int64_t)pc.c * kTileKeys);
+  if (!find_piece(p, piece, pc)) return;
+  while (pc.at < pc.end) {
+  const Part pt = part_of(p, pc);
+  advance(p, pt, pc);
+  const int len = pt.rng.len, lo = pt.rng.lo, first = pt.first, last = pt.last;
 
+  const bool tile_live = (rg * RT + rt) * 16 < p.rows;
   const int row = (rg * RT + rt) * 16 + col;
   const bool row_live = row < p.rows;
   const int tok = row_live ? row / p.group : 0;
   const int head = row_live ? h * p.group + row - tok * p.group : 0;
-  const int64_t qrow = (int64_t)pc.b * p.q_len + tok;
+  const int64_t qrow = (int64_t)pt.b * p.q_len + tok;
   const int row_hi = len - p.q_len + 1 + tok;
   const int row_lo = p.window > 0 ? row_hi - p.window : 0;
   const int all_hi = len - p.q_len + 1;
@@ -512,20 +579,14 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   for (int b = 0; b < NB; ++b) o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = kNoMax, l = 0.f;
 
-  const int32_t* trow = p.table + (int64_t)pc.b * p.table_width;
+  Pages pages(p, pt);
   const int page_mask = (1 << p.page_shift) - 1;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-  // a wave stages rows wave * KT / 4 .. of a step, in one 16-key tile and so one page
-  constexpr int WR = KT / 4;                  // rows per wave
+  // a wave stages rows wave * WR .. of a step, in one 16-key tile and so one page
+  constexpr int WR = 32 / RT;                 // rows per wave
   constexpr int RI = WR / LD;                 // rows per load of the wave
   static_assert(16 % WR == 0 && RI * LD == WR, "a wave's rows stay in one page");
-  // page of the wave's rows, or -1: no key of them is read
-  auto page_at = [&](int key0) {
-    const int kt = (key0 + wave * WR) & ~15;
-    if (!(kt < len && kt + 16 > lo)) return -1;
-    const int pid = entry(trow, kt >> p.page_shift);
-    return pid >= 0 && pid < p.pages ? pid : -1;
-  };
+  bool have[2], have_next[2];                 // whether the wave's two tiles of a step have keys
   u32x2 reg[FP8 ? NT : 1][FP8 ? LD : 1];      // FP8: codes of a step on their way
   uint32_t rsc[FP8 ? NT : 1][FP8 ? LD : 1];   // and their scale bytes
   // the chunk of its row that belongs at this lane's place of tile row tr
@@ -533,8 +594,10 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   auto fetch = [&](int buf, int key0) {
     int sr = lane / C % RI, sc = lane % C;    // row among a load's, chunk of it
     asm volatile("" : "+v"(sr), "+v"(sc));    // as below: no places kept over the loop
-    const int pid = page_at(key0);
     const int kr = key0 + wave * WR;          // the wave's first key
+    const int pid = pages.at(p, kr);
+    have_next[0] = pages.at(p, key0 + 32 * kp) >= 0;
+    have_next[1] = pages.at(p, key0 + 32 * kp + 16) >= 0;
     const int64_t off = (int64_t)max(pid, 0) * p.sp + h * p.sh + (int64_t)(kr & page_mask) * p.st;
     const int64_t srow = (((int64_t)max(pid, 0) * p.hkv + h) << p.page_shift) + (kr & page_mask);
     const int ra = pid >= 0 ? max(lo - kr, 0) : 0;                // rows [ra, rz) are read;
@@ -600,6 +663,8 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   int buf = 0;
   for (int key0 = first; key0 < last; key0 += KT, buf ^= 1) {
     const bool more = key0 + KT < last;
+    have[0] = have_next[0];
+    have[1] = have_next[1];
     if (more) fetch(buf ^ 1, key0 + KT);
     const int mykey = key0 + 32 * kp;
     // LDS places of this lane's chunks: kv_at's permutation is an exclusive or,
@@ -610,17 +675,10 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
     int ka = buf * TB + kv_at<D>(32 * kp + col, g);
     int va = (ONE ? 0 : 2 * TB) + buf * TB + kv_at<D>(vr, (col & 3) >> 1) + (col & 1) * 8;
     asm volatile("" : "+v"(ka), "+v"(va));
-    if (KP == 1 || mykey < last) {
+    if (tile_live && (KP == 1 || mykey < last)) {
       f32x4 s[2];
-      bool have[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int k16 = mykey + 16 * t;
-        have[t] = k16 < len && k16 + 16 > lo;
-        const int pid = have[t] ? entry(trow, k16 >> p.page_shift) : -1;
-        have[t] = pid >= 0 && pid < p.pages;
-        s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
+      for (int t = 0; t < 2; ++t) s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NF; ++j)
 #pragma unroll
@@ -643,8 +701,7 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
       float mx = pr[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, pr[i]);
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      mx = quarters_max(mx);
       if (__ballot(mx > m + kLag)) {
         const float mn = fmaxf(m, mx);
         const float a = exp2_fast(m - mn);
@@ -673,11 +730,12 @@ __global__ __launch_bounds__(256, (ONE || D < 512) ? 2 : 1) void attn_decode_row
   l += __shfl_xor(l, 32);
   if constexpr (KP > 1) {
     join_waves<KP, RT, NB>(reinterpret_cast<float*>(lds), kp, rt, m, l, o);
-    if (kp > 0) return;
+    if (kp > 0) continue;
   }
   finish<D, NB>(
-      p, pc, slot, h, rg, row, row_live, qrow, head, g, m, l,
+      p, pt, h, rg, row, row_live, qrow, head, g, m, l,
       [&](int i) { return 16 * i + 4 * g; }, [&](int i) { return o[i]; });
+  }
 }
 
 // Joins the splits of a sequence: one workgroup per (sequence, head, row);
@@ -730,20 +788,21 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
     p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
-// Row tiles of a workgroup.  Two tiles leave two waves to share each, which
-// doubles a step's keys: 512-element heads have no LDS for that.
-int row_tiles(int rows, int dim) { return rows <= 16 ? 1 : rows <= 32 && dim < 512 ? 2 : 4; }
+// Row tiles of a workgroup; 1: the kernel without LDS.  512-element heads have
+// no registers for that one, and no LDS for the twofold step of two tiles.
+int row_tiles(int rows, int dim) { return dim == 512 ? 4 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 struct DecodePlan {
-  int rows, rgroups, target, slots;
+  int rows, rgroups, pieces;
+  int64_t slots;
 };
 DecodePlan plan_of(const moe_attn_config& c) {
   DecodePlan d;
   d.rows = c.q_len * (c.heads_q / c.heads_kv);
   const int rt = row_tiles(d.rows, c.head_dim);
   d.rgroups = (d.rows + 16 * rt - 1) / (16 * rt);
-  d.target = std::max(1, (rt == 1 ? kSplitTarget : kSplitTargetRows) / (c.heads_kv * d.rgroups));
-  d.slots = d.target + c.batch;
+  d.pieces = std::max(1, (rt == 1 ? kPieces : kPiecesRows) / (c.heads_kv * d.rgroups));
+  d.slots = (int64_t)d.pieces + c.batch;
   return d;
 }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -774,7 +833,8 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.page_shift = __builtin_ctz((unsigned)kv.page_size);
   a.batch = c.batch; a.q_len = c.q_len; a.hq = c.heads_q; a.hkv = c.heads_kv;
   a.group = c.heads_q / c.heads_kv;
-  a.rows = d.rows; a.rgroups = d.rgroups; a.target = d.target; a.slots = d.slots;
+  a.rows = d.rows; a.rgroups = d.rgroups; a.pieces = d.pieces;
+  a.tile_shift = row_tiles(d.rows, c.head_dim) == 1 ? 7 : 6;
   a.window = c.window; a.scale2 = c.scale * kLog2e;
   const size_t rows = (size_t)d.slots * c.heads_kv * d.rows;
   char* w = static_cast<char*>(ws);
@@ -782,30 +842,37 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.part_m = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.part_l = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.meta = reinterpret_cast<int2*>(w);
-  const dim3 grid((unsigned)d.slots * c.heads_kv * d.rgroups);
+  const dim3 grid((unsigned)(d.pieces * c.heads_kv * d.rgroups));
   const int rt = row_tiles(d.rows, c.head_dim);
   const bool f8 = kv.format == MOE_KV_FP8;
   const bool one = kv.k == kv.v;
-#define MOE_ROWS(D, F, R, O) \
-  hipLaunchKernelGGL((attn_decode_rows_kernel<D, F, R, O>), grid, dim3(256), 0, st, a)
-#define MOE_ROWS_F(D, F)                                                                      \
+#define MOE_ROWS(D, F, R, KP, O)                                                              \
+  hipLaunchKernelGGL((attn_decode_rows_kernel<D, F, R, KP, O>), grid, dim3(64 * R * KP), 0, st, a)
+#define MOE_ROWS_ANY(D, F, R)                                                                 \
+  do {                                                                                        \
+    if (one) MOE_ROWS(D, F, R, (D == 512 ? 2 : 4 / R), true);                                 \
+    else MOE_ROWS(D, F, R, 4 / R, false);                                                     \
+  } while (0)
+#define MOE_FEW(D, F)                                                                         \
   do {                                                                                        \
     if (rt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, F>), grid, dim3(256), 0, st, a);   \
-    else if (rt == 2 && one) MOE_ROWS(D, F, (D < 512 ? 2 : 4), true);                         \
-    else if (rt == 2) MOE_ROWS(D, F, (D < 512 ? 2 : 4), false);                               \
-    else if (one) MOE_ROWS(D, F, 4, true);                                                    \
-    else MOE_ROWS(D, F, 4, false);                                                            \
+    else if (rt == 2) MOE_ROWS_ANY(D, F, 2);                                                  \
+    else MOE_ROWS_ANY(D, F, 4);                                                               \
   } while (0)
 #define MOE_DECODE(D)                                                                         \
   case D:                                                                                     \
-    if (f8) MOE_ROWS_F(D, true); else MOE_ROWS_F(D, false);                                   \
+    if (f8) MOE_FEW(D, true); else MOE_FEW(D, false);                                         \
     break;
   switch (c.head_dim) {
-    MOE_DECODE(64) MOE_DECODE(128) MOE_DECODE(256) MOE_DECODE(512)
+    MOE_DECODE(64) MOE_DECODE(128) MOE_DECODE(256)
+    case 512:
+      if (f8) MOE_ROWS_ANY(512, true, 4); else MOE_ROWS_ANY(512, false, 4);
+      break;
     default: return hipErrorInvalidValue;
   }
 #undef MOE_DECODE
-#undef MOE_ROWS_F
+#undef MOE_FEW
+#undef MOE_ROWS_ANY
 #undef MOE_ROWS
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

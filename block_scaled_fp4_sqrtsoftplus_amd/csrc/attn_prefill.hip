@@ -65,12 +65,7 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& p, int tile, Seq& s
           p.group;
       n = (int)((rows + BM - 1) / BM);
     }
-    int incl = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
+    const int incl = wave_scan(n);
     const uint64_t past = __ballot(base + incl > tile);
     if (past) {
       const int l = __builtin_ctzll(past);

@@ -131,7 +131,8 @@ size_t moe_attn_workspace_size(const moe_attn_config* cfg);
  *   q, out       [batch * q_len, heads_q, head_dim]
  *   block_table  [batch, table_width] int32 pages; entries that no row's mask
  *                reaches are not read; keys on a page outside [0, pages) are
- *                left out
+ *                left out; table_width * page_size at most 2^30, and times
+ *                batch below 2^36
  *   seq_lens     [batch] int32, new tokens included; less than 1 keeps
  *                nothing, more than table_width * page_size is that
  *   lse          [batch * q_len, heads_q] fp32 or NULL
