@@ -58,34 +58,48 @@ def _stream(device):
     return _raw_stream(device.index)
 
 
-def _on(t, device, name):
-    """The address of a contiguous tensor on `device`."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-    return _ptr(t)
+_bf16, _int32, _int64 = torch.bfloat16, torch.int32, torch.int64
 
 
-def _rows(t, tokens, heads, dim, device, name):
-    """MoeRowsC of a [tokens, heads, dim] bf16 tensor."""
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be bfloat16")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU that holds the call's other tensors")
-    if t.shape != (tokens, heads, dim):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, dim)}")
-    st = t.stride()
-    if st[2] != 1:
-        raise ValueError(f"{name}: the last index must be contiguous")
-    # strides over indices of one value are free
-    return MoeRowsC(t.data_ptr() or None, st[0] if tokens > 1 else 0, st[1] if heads > 1 else 0)
-
-
-def _ints(t, dtype, shape, device, name):
+def _refuse(t, dtype, shape, device, name):
+    """Raises for what is wrong with an argument."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return _on(t, device, name)
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the HIP library must be on the GPU")
+    raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+
+
+# The checks below run on every call of a decode step, where the host's time
+# is what a small call costs: one test for all that is usual, the reasons apart.
+
+
+def _rows(t, tokens, heads, dim, device, name):
+    """MoeRowsC of a [tokens, heads, dim] bf16 tensor on the GPU `device`."""
+    if t.dtype is not _bf16 or t.shape != (tokens, heads, dim) or t.device != device:
+        _refuse(t, _bf16, (tokens, heads, dim), device, name)
+    st, sh, se = t.stride()
+    if se != 1:
+        raise ValueError(f"{name}: the last index must be contiguous")
+    # strides over indices of one value are free
+    return MoeRowsC(t.data_ptr() or None, st if tokens > 1 else 0, sh if heads > 1 else 0)
+
+
+def _new_rows(tokens, heads, dim, device):
+    """A new [tokens, heads, dim] bf16 tensor and its MoeRowsC."""
+    t = torch.empty((tokens, heads, dim), dtype=_bf16, device=device)
+    return t, MoeRowsC(t.data_ptr() or None, heads * dim, dim)
+
+
+def _ints(t, dtype, shape, device, name):
+    """The address of a contiguous tensor on the GPU `device`."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse(t, dtype, shape, device, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or _ptr(t)
 
 
 class KVCache:
@@ -175,8 +189,8 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope: Rope = None, q=
     tokens, heads, dim, dev = k.shape[0], cache.heads, cache.head_dim, cache.device
     kc = _rows(k, tokens, heads, dim, dev, "k")
     vc = _byref(_rows(v, tokens, heads, dim, dev, "v")) if v is not None else None
-    sl = _ints(slots, torch.int64, (tokens,), dev, "slots")
-    ps = _ints(positions, torch.int32, (tokens,), dev, "positions") if positions is not None else None
+    sl = _ints(slots, _int64, (tokens,), dev, "slots")
+    ps = _ints(positions, _int32, (tokens,), dev, "positions") if positions is not None else None
     if rope is not None and rope.device != dev:
         raise ValueError("rope is on another device than the cache")
     qc = oc = None
@@ -185,8 +199,10 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope: Rope = None, q=
         hq = q.shape[1]
         qc = _byref(_rows(q, tokens, hq, dim, dev, "q"))
         if q_out is None:
-            q_out = torch.empty((tokens, hq, dim), dtype=torch.bfloat16, device=dev)
-        oc = _byref(_rows(q_out, tokens, hq, dim, dev, "q_out"))
+            q_out, oc = _new_rows(tokens, hq, dim, dev)
+        else:
+            oc = _rows(q_out, tokens, hq, dim, dev, "q_out")
+        oc = _byref(oc)
     elif q_out is not None:
         raise ValueError("q_out without q")
     ko = _byref(_rows(k_out, tokens, heads, dim, dev, "k_out")) if k_out is not None else None
@@ -223,13 +239,14 @@ class DecodeAttention:
         cache, n, dev = self.cache, self.tokens, self.cache.device
         qc = _rows(q, n, self.heads_q, cache.head_dim, dev, "q")
         if out is None:
-            out = torch.empty((n, self.heads_q, cache.head_dim), dtype=torch.bfloat16, device=dev)
-        oc = _rows(out, n, self.heads_q, cache.head_dim, dev, "out")
+            out, oc = _new_rows(n, self.heads_q, cache.head_dim, dev)
+        else:
+            oc = _rows(out, n, self.heads_q, cache.head_dim, dev, "out")
         if block_table.dim() != 2:
             raise ValueError("block_table must be [batch, width]")
         width = block_table.shape[1]
-        bt = _ints(block_table, torch.int32, (self.batch, width), dev, "block_table")
-        sl = _ints(seq_lens, torch.int32, (self.batch,), dev, "seq_lens")
+        bt = _ints(block_table, _int32, (self.batch, width), dev, "block_table")
+        sl = _ints(seq_lens, _int32, (self.batch,), dev, "seq_lens")
         lse = torch.empty((n, self.heads_q), dtype=torch.float32, device=dev) if want_lse else None
         _check(lib.moe_attn_decode(self._ref, _byref(qc), cache._ref, bt, width, sl, _byref(oc),
                                    lse.data_ptr() if want_lse else None, self._ws, self.ws_bytes, _stream(dev)))
@@ -248,6 +265,8 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal=True, window=0, scale=None, ou
     [tokens, heads_q] fp32."""
     if q.dim() != 3 or k.dim() != 3 or cu_q.dim() != 1:
         raise ValueError("q, k and v must be [tokens, heads, head_dim], cu_q [sequences + 1]")
+    if not q.is_cuda:
+        raise ValueError("tensors passed to the HIP library must be on the GPU")
     (tokens, hq, dim), (keys, hkv, _), dev = q.shape, k.shape, q.device
     if cu_q.shape[0] < 1:
         raise ValueError("cu_q has sequences + 1 entries")
@@ -256,11 +275,12 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal=True, window=0, scale=None, ou
     qc, kc = _rows(q, tokens, hq, dim, dev, "q"), _rows(k, keys, hkv, dim, dev, "k")
     vc = kc if v is k else _rows(v, keys, hkv, dim, dev, "v")
     batch = cu_q.shape[0] - 1
-    cq = _ints(cu_q, torch.int32, (batch + 1,), dev, "cu_q")
-    ck = _ints(cu_k, torch.int32, (batch + 1,), dev, "cu_k") if cu_k is not None else None
+    cq = _ints(cu_q, _int32, (batch + 1,), dev, "cu_q")
+    ck = _ints(cu_k, _int32, (batch + 1,), dev, "cu_k") if cu_k is not None else None
     if out is None:
-        out = torch.empty((tokens, hq, dim), dtype=torch.bfloat16, device=dev)
-    oc = _rows(out, tokens, hq, dim, dev, "out")
+        out, oc = _new_rows(tokens, hq, dim, dev)
+    else:
+        oc = _rows(out, tokens, hq, dim, dev, "out")
     lse = torch.empty((tokens, hq), dtype=torch.float32, device=dev) if want_lse else None
     c = MoeAttnConfigC(tokens, keys, batch, 1, hq, hkv, dim, int(causal), window,
                        dim ** -0.5 if scale is None else scale)

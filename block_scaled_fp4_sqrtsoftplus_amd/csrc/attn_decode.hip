@@ -49,7 +49,7 @@ struct DecodeArgs {
   int batch, q_len, hq, hkv, group, rows, rgroups;
   int window;
   float scale2;            // scale * log2(e)
-  int pieces;              // the work's, for one head and row group
+  int pieces;              // the work's, for one head and row group; 0: one per sequence
   int tile_shift;          // keys per tile, the unit of the cut: 2^tile_shift
   float* part_o;           // [pieces + batch][hkv][rows][D]
   float* part_m;           // [pieces + batch][hkv][rows] maximum (base 2)
@@ -96,6 +96,16 @@ struct Piece {
 // Every wave works its piece out for itself, 64 sequences at a time.
 __device__ __forceinline__ bool find_piece(const DecodeArgs& p, int w, Piece& out) {
   const int lane = threadIdx.x & 63;
+  if (p.pieces == 0) {                 // nothing is cut: piece w is sequence w
+    out.w = 0;
+    out.per = 1u << 30;
+    out.b = w;
+    out.tile = 0;
+    out.len = entry(p.seq_lens, w);
+    out.at = 0;
+    out.end = range_of(p, out.len).tiles;
+    return true;
+  }
   uint32_t total = 0;   // the host has checked that it stays below 2^31
   int raw = 0, mine = 0, incl = 0;   // the last 64 sequences looked at
   auto look = [&](int b0) {
@@ -796,6 +806,10 @@ struct DecodePlan {
   int rows, rgroups, pieces;
   int64_t slots;
 };
+// Sequences of no more keys than this are not cut: a workgroup takes
+// one in at most 4 steps, and the call is one kernel (measured for one
+// sequence of 300 keys: @@).
+constexpr int64_t kWholeKeys = 512;
 DecodePlan plan_of(const moe_attn_config& c) {
   DecodePlan d;
   d.rows = c.q_len * (c.heads_q / c.heads_kv);
@@ -833,7 +847,9 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.page_shift = __builtin_ctz((unsigned)kv.page_size);
   a.batch = c.batch; a.q_len = c.q_len; a.hq = c.heads_q; a.hkv = c.heads_kv;
   a.group = c.heads_q / c.heads_kv;
-  a.rows = d.rows; a.rgroups = d.rgroups; a.pieces = d.pieces;
+  a.rows = d.rows; a.rgroups = d.rgroups;
+  const bool whole = ((int64_t)table_width << a.page_shift) <= kWholeKeys;
+  a.pieces = whole ? 0 : d.pieces;
   a.tile_shift = row_tiles(d.rows, c.head_dim) == 1 ? 7 : 6;
   a.window = c.window; a.scale2 = c.scale * kLog2e;
   const size_t rows = (size_t)d.slots * c.heads_kv * d.rows;
@@ -842,7 +858,7 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.part_m = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.part_l = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.meta = reinterpret_cast<int2*>(w);
-  const dim3 grid((unsigned)(d.pieces * c.heads_kv * d.rgroups));
+  const dim3 grid((unsigned)((whole ? c.batch : d.pieces) * c.heads_kv * d.rgroups));
   const int rt = row_tiles(d.rows, c.head_dim);
   const bool f8 = kv.format == MOE_KV_FP8;
   const bool one = kv.k == kv.v;
@@ -875,7 +891,7 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
 #undef MOE_ROWS_ANY
 #undef MOE_ROWS
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || whole) return e;
   const dim3 jgrid((unsigned)((int64_t)c.batch * c.heads_kv * d.rows));
 #define MOE_JOIN(D) \
   case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), jgrid, dim3(256), 0, st, a); break;
