@@ -75,7 +75,7 @@ __device__ __forceinline__ bf16x8 read_tr(const char* a, const char* b) {
 __device__ __forceinline__ void load_lds16(uint32_t to, const char* base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(to), "v"(off), "s"(base)
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base)
                : "memory");
 }
 

@@ -84,20 +84,17 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& p, int tile, Seq& s
   return false;
 }
 
-// 16-byte chunk c of row r of a K or V tile in LDS: the position inside the row is permuted
-// so that the reads below touch every bank once.  K: a wave reads one chunk
-// of 32 rows.  V: the transposing read takes 4 chunks of 4 rows.
-
 // 16-byte chunk c of row r of a K or V tile in LDS sits at chunk c ^ swz(r) of
 // the row, so that the reads below touch every bank once.  K: 16 lanes read
 // one chunk of 16 rows.  V: the transposing read takes 4 chunks of 4 rows.
+// 512-element heads have one permutation for both, so that a tile may be both.
 template <int D>
 __device__ __forceinline__ int k_swz(int r) {
-  return D == 64 ? (r >> 1) & 7 : r & 15;
+  return D == 64 ? (r >> 1) & 7 : D == 512 ? ((r & 3) << 2) | ((r >> 2) & 3) : r & 15;
 }
 template <int D>
 __device__ __forceinline__ int v_swz(int r) {
-  return D == 64 ? 4 * ((r >> 1) & 1) : 4 * (r & 3);
+  return D == 64 ? 4 * ((r >> 1) & 1) : D == 512 ? k_swz<D>(r) : 4 * (r & 3);
 }
 template <int D>
 __device__ __forceinline__ int k_at(int r, int c) {
@@ -111,10 +108,10 @@ __device__ __forceinline__ int v_at(int r, int c) {
 // RG row groups of 32 rows; SPLIT waves share a group (each has a D / SPLIT
 // slice of both products' columns, and they add their parts of S through
 // LDS).  BN: keys per step.  BUFS: LDS tiles of K and of V, BUFS - 1 of them on
-// their way while one is read.  PIPE: a step takes the weights of its scores while the matrix
+// their way while one is read (with ONE, where v is k, of the one tensor: three).  PIPE: a step takes the weights of its scores while the matrix
 // units take the next step's scores.  AHEAD: products by which LDS reads run
 // ahead of their use.  WAVES: waves per SIMD that the registers are held to.
-template <int D, int BN, int RG, int SPLIT, int BUFS, bool PIPE, int AHEAD, int WAVES>
+template <int D, int BN, int RG, int SPLIT, int BUFS, bool PIPE, int AHEAD, int WAVES, bool ONE>
 __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(PrefillArgs p) {
   constexpr int BM = 32 * RG;
   constexpr int TH = 64 * RG * SPLIT;
@@ -124,8 +121,8 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   constexpr int C = D / 8;                   // 16-byte chunks per row
   constexpr int LD = BN * C / TH;            // chunks a thread stages per tensor
   constexpr int TB = BN * D * 2;             // bytes of one tile
-  constexpr int V0 = BUFS * TB;              // the tiles of V
-  constexpr int X0 = 2 * BUFS * TB;          // the waves' parts of S
+  constexpr int V0 = ONE ? 0 : BUFS * TB;    // the tiles of V
+  constexpr int X0 = (ONE ? BUFS : 2 * BUFS) * TB;   // the waves' parts of S
   constexpr int XB = SPLIT > 1 ? RG * SPLIT * NK * 4096 : 0;
   __shared__ __align__(16) char lds[X0 + XB];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -194,9 +191,10 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   const char* kb = reinterpret_cast<const char*>(p.k + s.k0 * p.k_st + h * p.k_sh);
   const char* vb = reinterpret_cast<const char*>(p.v + s.k0 * p.v_st + h * p.v_sh);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-  const int r0 = tid / C, c0 = tid % C;
+  int r0 = tid / C, c0 = tid % C;
   // chunk i of a tile whose rows are all keys
   auto fetch_one = [&](int which, int buf, int key0, int i) {
+    if constexpr (D == 512) asm volatile("" : "+v"(r0), "+v"(c0));   // no places kept over the loop
     const int64_t st = 2 * (which ? p.v_st : p.k_st);
     const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
     load_lds16(lds0 + (which ? V0 : 0) + buf * TB + wv * 1024 + i * TH * 16,
@@ -234,9 +232,9 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   };
   auto read_v = [&](int va, int i) {   // operand of PV product i: keys i / ND, columns i % ND
     const int ch = 4 * (i % ND);       // chunk 4 (part ND + ..) of rows 16 (i / ND) + .. and 8 below
-    const char* v0 = lds + (va ^ ((ch & 15) * 16)) + (ch & ~15) * 16 + part * ND * 64 +
-                     16 * (i / ND) * D * 2;
-    return read_tr(v0, v0 + 8 * D * 2);
+    const int at = va ^ ((ch & 15) * 16);
+    const char* v0 = lds + (ch & ~15) * 16 + part * ND * 64 + 16 * (i / ND) * D * 2;
+    return read_tr(v0 + at, v0 + (at ^ (v_swz<D>(8) * 16)) + 8 * D * 2);
   };
   float* xs = reinterpret_cast<float*>(lds + X0);
   auto hand_over = [&](const f32x16(&sc)[NK]) {   // SPLIT 2: this wave's part for the other
@@ -246,9 +244,9 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<f32x4*>(xs + ((wv * NK + t) * 4 + i / 4) * 256 + lane * 4) =
             f32x4{sc[t][i], sc[t][i + 1], sc[t][i + 2], sc[t][i + 3]};
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
   };
   auto take_over = [&](f32x16(&sc)[NK]) {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
@@ -377,8 +375,8 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       int ka = kb_next * TB + k_lane, va = V0 + vb_now * TB + v_lane;
       asm volatile("" : "+v"(ka), "+v"(va));
       auto read = [&](int i) { return i < QK ? read_k(ka, i) : read_v(va, i - QK); };
-      constexpr int PER = NE / QK;
-      static_assert(PER * QK == NE, "");
+      // the elements behind product i
+      auto from = [](int i) { return (i < 0 ? 0 : i) * NE / QK; };
 #pragma unroll
       for (int t = 0; t < NK; ++t)
 #pragma unroll
@@ -390,12 +388,13 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       for (int i = 0; i < QK; ++i) {
         nx[i % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD], qf[i / NK], nx[i % NK], 0, 0, 0);
         f[i % AHEAD] = read(i + AHEAD);
+        // three products' elements at once, so that no part waits for the one before it
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {      // three products' elements at once: no part waits
-          if (i >= 2) weight_sum(sc, (i - 2) * PER + e);
-          if (i >= 1) weight_exp(sc, (i - 1) * PER + e);
-          weight_arg(sc, i * PER + e);
-        }
+        for (int e = from(i - 2); e < from(i - 1); ++e) weight_sum(sc, e);
+#pragma unroll
+        for (int e = from(i - 1); e < from(i); ++e) weight_exp(sc, e);
+#pragma unroll
+        for (int e = from(i); e < from(i + 1); ++e) weight_arg(sc, e);
         if constexpr (WHOLE) {
 #pragma unroll
           for (int j = i * 2 * LD / QK; j < (i + 1) * 2 * LD / QK; ++j) {
@@ -406,7 +405,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int e = (QK - 1) * PER; e < NE; ++e) weight_exp(sc, e);
+      for (int e = from(QK - 1); e < NE; ++e) weight_exp(sc, e);
       if constexpr (SPLIT == 2) hand_over(nx);
       float mx[4];
 #pragma unroll
@@ -416,7 +415,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
         if (i + AHEAD < PV) f[(QK + i) % AHEAD] = read(QK + i + AHEAD);
         if (i < 2) {                         // the last two products' weights
 #pragma unroll
-          for (int e = 0; e < PER; ++e) weight_sum(sc, (QK - 2 + i) * PER + e);
+          for (int e = from(QK - 2 + i); e < from(QK - 1 + i); ++e) weight_sum(sc, e);
         }
         if constexpr (WHOLE && SPLIT == 1) {
 #pragma unroll
@@ -458,6 +457,60 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       for (int e = 0; e < NE; ++e) weight(sc, e);
       values(vb_now);
     }
+  } else if constexpr (SPLIT == 2) {
+    // The product with V lags a step behind, so that it runs while the waves'
+    // parts of S pass through LDS.  Tiles of K take turns in kb, kb_next .., the
+    // lagging tile of V is vb; with ONE that is K's of the step before.
+    f32x16 sc[NK];
+    int kb = 0, vb = 0;
+    if (steps > 0) fetch(0, 0, key_lo);
+    step_barrier<0>();
+    auto step = [&](int it, auto first) {
+      constexpr bool LAG = !decltype(first)::value;
+      const int key0 = key_lo + it * BN;
+      const int kb_next = kb + 1 == (ONE ? 3 : 2) ? 0 : kb + 1;
+      const int vb_next = ONE ? kb : vb ^ 1;
+      if (it + 1 < steps) fetch(0, kb_next, key0 + BN);
+      if constexpr (!ONE) fetch(1, vb_next, key0);
+      int ka = kb * TB + k_lane, va = V0 + vb * TB + v_lane;
+      asm volatile("" : "+v"(ka), "+v"(va));
+      auto read = [&](int i) { return i < QK ? read_k(ka, i) : read_v(va, i - QK); };
+      constexpr int N = LAG ? QK + PV : QK;
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[t][i] = 0.f;
+      bf16x8 f[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) f[i] = read(i);
+#pragma unroll
+      for (int i = 0; i < QK; ++i) {
+        sc[i % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % AHEAD], qf[i / NK], sc[i % NK], 0, 0, 0);
+        if (i + AHEAD < N) f[i % AHEAD] = read(i + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      hand_over(sc);
+#pragma unroll
+      for (int i = QK; i < N; ++i) {
+        o[(i - QK) % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            f[i % AHEAD], __builtin_bit_cast(bf16x8, pw[(i - QK) / ND]), o[(i - QK) % ND], 0, 0, 0);
+        if (i + AHEAD < N) f[i % AHEAD] = read(i + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      take_over(sc);
+      if (!inner(key0)) mask(key0, sc);
+      raise(largest(sc));
+#pragma unroll
+      for (int e = 0; e < NE; ++e) weight(sc, e);
+      kb = kb_next;
+      vb = vb_next;
+      step_barrier<0>();
+    };
+    if (steps > 0) {
+      step(0, std::true_type{});
+      for (int it = 1; it < steps; ++it) step(it, std::false_type{});
+      values(vb);
+    }
   } else {
     if (steps > 0) {
       fetch(0, 0, key_lo);
@@ -473,10 +526,6 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       }
       f32x16 sc[NK];
       scores(buf, sc);
-      if constexpr (SPLIT == 2) {
-        hand_over(sc);
-        take_over(sc);
-      }
       if (!inner(key0)) mask(key0, sc);
       raise(largest(sc));
 #pragma unroll
@@ -522,19 +571,24 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
   a.causal = c.causal; a.window = c.window;
   a.q_flip = c.scale < 0.f ? 0x80008000u : 0u;
   a.scale2 = (c.scale < 0.f ? -c.scale : c.scale) * kLog2e;
-#define MOE_PREFILL(D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES)                               \
-  case D: {                                                                                   \
+#define MOE_PREFILL(D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES, ONE)                          \
+  {                                                                                           \
     /* at most one partly filled tile per sequence */                                         \
     const int64_t tiles = c.tokens * a.group / (32 * RG) + std::min<int64_t>(c.batch, c.tokens); \
-    hipLaunchKernelGGL((attn_prefill_kernel<D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES>),            \
+    hipLaunchKernelGGL((attn_prefill_kernel<D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES, ONE>),            \
                        dim3((unsigned)(tiles * c.heads_kv)), dim3(64 * RG * SPLIT), 0, st, a); \
     break;                                                                                    \
   }
   switch (c.head_dim) {
-    MOE_PREFILL(64, 64, 4, 1, 2, false, 4, 2)
-    MOE_PREFILL(128, 64, 4, 1, 2, true, 3, 2)
-    MOE_PREFILL(256, 32, 4, 1, 3, true, 2, 2)
-    MOE_PREFILL(512, 32, 4, 2, 2, false, 2, 2)
+    case 64: MOE_PREFILL(64, 64, 4, 1, 2, false, 4, 2, false)
+    case 128: MOE_PREFILL(128, 64, 4, 1, 2, true, 3, 2, false)
+    case 256: MOE_PREFILL(256, 32, 4, 1, 3, true, 2, 2, false)
+    case 512:
+      if (v.p == k.p && v.stride_token == k.stride_token && v.stride_head == k.stride_head)
+        MOE_PREFILL(512, 32, 4, 2, 3, false, 2, 2, true)
+      else
+        MOE_PREFILL(512, 32, 4, 2, 2, false, 2, 2, false)
+      break;
     default: return hipErrorInvalidValue;
   }
 #undef MOE_PREFILL
