@@ -28,9 +28,14 @@ namespace moe {
 
 namespace {
 
-// Workgroups the tiles are dealt to, by the kernel that takes them.
+// Pieces the work is cut into: two workgroups a CU for the kernel without LDS
+// (of 256, 512, 768 and 1024 pieces the best or within 1% of it for 64 ragged
+// sequences, one long one and 256-element heads).  The one with LDS has one
+// workgroup a CU, and its own cut adds up to a piece per sequence: together
+// they stay below the CUs, since a second round doubles the time (85 instead
+// of 60 us at 32 sequences on one 512-element head).
 constexpr int kPieces = 512;
-constexpr int kPiecesRows = 256;
+int pieces_rows(int batch) { return std::max(256 - batch, 128); }
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -81,12 +86,17 @@ __device__ __forceinline__ Range range_of(const DecodeArgs& p, int raw_len) {
   return r;
 }
 
-// The work of all sequences, laid end to end in tiles, is cut into pieces of
-// equal length, one per workgroup (of a head and row group); a piece covers
-// the end of a sequence, whole ones and the start of another.  An empty sequence
-// counts a tile, so that a piece writes its rows.  Sequence b's part of piece w
-// is a split with slot w + b: every step along the work raises one of the two,
-// so slots differ, and those of a sequence are consecutive.
+// The work of all sequences, laid end to end in tiles, is cut into pieces, one
+// per workgroup (of a head and row group).  An empty sequence counts a tile,
+// so that a piece writes its rows.
+// ACROSS: pieces of equal length; one covers the end of a sequence, whole ones and
+// the start of another.  Sequence b's part of piece w is a split with slot w +
+// b: every step along the work raises one of the two, so slots differ, and
+// those of a sequence are consecutive.
+// Otherwise each sequence is cut by itself into pieces of at most the same
+// length, which are its splits and slots: more uneven, but a part of a
+// sequence costs the kernel for many rows as much as 200 keys (its rows of q, its first
+// tiles, its partial result).
 struct Piece {
   int w;            // piece
   uint32_t per;     // tiles per piece
@@ -94,6 +104,7 @@ struct Piece {
   int b, tile, len; // the sequence of the first one, the tile's place there, seq_lens[b]
 };
 // Every wave works its piece out for itself, 64 sequences at a time.
+template <bool ACROSS>
 __device__ __forceinline__ bool find_piece(const DecodeArgs& p, int w, Piece& out) {
   const int lane = threadIdx.x & 63;
   if (p.pieces == 0) {                 // nothing is cut: piece w is sequence w
@@ -118,7 +129,29 @@ __device__ __forceinline__ bool find_piece(const DecodeArgs& p, int w, Piece& ou
     total += __builtin_amdgcn_readlane(incl, 63);
   }
   out.w = w;
-  out.per = (total + p.pieces - 1) / p.pieces;
+  out.per = __builtin_amdgcn_readfirstlane((total + p.pieces - 1) / p.pieces);
+  if constexpr (!ACROSS) {
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 64) {
+      if (p.batch > 64) look(b0);
+      const int n = (int)((mine + out.per - 1) / out.per);   // 0 past the last sequence
+      incl = wave_scan(n);
+      const uint64_t past = __ballot(base + incl > (uint32_t)w);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        out.b = __builtin_amdgcn_readfirstlane(b0 + l);
+        out.len = __builtin_amdgcn_readlane(raw, l);
+        out.tile = __builtin_amdgcn_readfirstlane(
+            (w - (int)(base + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l))) *
+            (int)out.per);
+        out.at = out.tile;
+        out.end = min(out.at + out.per, (uint32_t)__builtin_amdgcn_readlane(mine, l));
+        return true;
+      }
+      base += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return false;
+  }
   out.at = (uint32_t)min((uint64_t)w * out.per, (uint64_t)total);
   out.end = min(out.at + out.per, total);
   if (out.at >= total) return false;
@@ -146,13 +179,15 @@ struct Part {
   Range rng;
   int first, last;  // keys
 };
+template <bool ACROSS>
 __device__ __forceinline__ Part part_of(const DecodeArgs& p, const Piece& pc) {
   Part x;
   x.b = pc.b;
-  x.slot = pc.w + pc.b;
+  x.slot = ACROSS ? pc.w + pc.b : pc.w;
   x.rng = range_of(p, pc.len);
-  const uint32_t begin = pc.at - pc.tile;   // the sequence's first tile in all the work
-  x.splits = (int)((begin + x.rng.tiles - 1) / pc.per - begin / pc.per) + 1;
+  const uint32_t begin = pc.at - pc.tile;   // the sequence's first tile in all the work, or 0
+  x.splits = __builtin_amdgcn_readfirstlane(
+      (int)((begin + x.rng.tiles - 1) / pc.per - begin / pc.per) + 1);
   x.starts = pc.tile == 0;
   const int n = min((int)(pc.end - pc.at), x.rng.tiles - pc.tile);
   x.first = (x.rng.lo & ~31) + (pc.tile << p.tile_shift);
@@ -294,9 +329,9 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
   const int h = blockIdx.x - piece * p.hkv;
   constexpr int rg = 0;
   Piece pc;
-  if (!find_piece(p, piece, pc)) return;
+  if (!find_piece<true>(p, piece, pc)) return;
   while (pc.at < pc.end) {
-  const Part pt = part_of(p, pc);
+  const Part pt = part_of<true>(p, pc);
   advance(p, pt, pc);
   const int len = pt.rng.len, lo = pt.rng.lo, first = pt.first, last = pt.last;
 
@@ -559,9 +594,9 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
   const int rest = blockIdx.x - piece * per_piece;
   const int rg = rest / p.hkv, h = rest - rg * p.hkv;
   Piece pc;
-  if (!find_piece(p, piece, pc)) return;
+  if (!find_piece<false>(p, piece, pc)) return;
   while (pc.at < pc.end) {
-  const Part pt = part_of(p, pc);
+  const Part pt = part_of<false>(p, pc);
   advance(p, pt, pc);
   const int len = pt.rng.len, lo = pt.rng.lo, first = pt.first, last = pt.last;
 
@@ -755,43 +790,53 @@ template <int D>
 __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
   constexpr int GL = D / 4, NGR = 256 / GL;
   __shared__ f32x4 so[NGR][GL];
-  __shared__ float sl[NGR];
-  const int64_t per_b = (int64_t)p.hkv * p.rows;
-  const int64_t b = blockIdx.x / per_b;
+  __shared__ float sm[NGR], sl[NGR];
+  const uint32_t per_b = (uint32_t)(p.hkv * p.rows);
+  const uint32_t b = blockIdx.x / per_b;
   const int rest = (int)(blockIdx.x - b * per_b);
   const int h = rest / p.rows, row = rest - h * p.rows;
   const int2 mt = p.meta[b];
   if (mt.y <= 1) return;
   const int64_t at0 = (int64_t)mt.x * per_b + (int64_t)h * p.rows + row;
-  const int lane = threadIdx.x & 63;
   const int gr = threadIdx.x / GL, gl = threadIdx.x % GL;
-  float m = kNoMax;
-  for (int i = lane; i < mt.y; i += 64) m = fmaxf(m, p.part_m[at0 + i * per_b]);
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+  // a group's own running maximum: no load waits for another's
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
+  float l = 0.f, m = kNoMax;
 #pragma unroll 4
   for (int i = gr; i < mt.y; i += NGR) {
-    const int64_t at = at0 + i * per_b;
-    const float a = exp2_fast(p.part_m[at] - m);
-    l += a * p.part_l[at];
-    o += a * *reinterpret_cast<const f32x4*>(p.part_o + at * D + gl * 4);
+    const int64_t at = at0 + (int64_t)i * per_b;
+    const float mi = p.part_m[at], li = p.part_l[at];
+    const f32x4 oi = *reinterpret_cast<const f32x4*>(p.part_o + at * D + gl * 4);
+    const float mn = fmaxf(m, mi);
+    const float a = exp2_fast(m - mn), c = exp2_fast(mi - mn);
+    m = mn;
+    l = l * a + li * c;
+    o = o * a + oi * c;
   }
   so[gr][gl] = o;
-  if (gl == 0) sl[gr] = l;
+  if (gl == 0) {
+    sm[gr] = m;
+    sl[gr] = l;
+  }
   __syncthreads();
   if (gr > 0) return;
+  float top = sm[0];
 #pragma unroll
-  for (int i = 1; i < NGR; ++i) {
-    o += so[i][gl];
-    l += sl[i];
+  for (int i = 1; i < NGR; ++i) top = fmaxf(top, sm[i]);
+  o = f32x4{0.f, 0.f, 0.f, 0.f};
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < NGR; ++i) {
+    const float a = exp2_fast(sm[i] - top);
+    o += so[i][gl] * a;
+    l += sl[i] * a;
   }
+  m = top;
   const float inv = l > 0.f ? 1.0f / l : 0.f;
   o *= inv;
   const int tok = row / p.group;
   const int head = h * p.group + row - tok * p.group;
-  const int64_t qrow = b * p.q_len + tok;
+  const int64_t qrow = (int64_t)b * p.q_len + tok;
   *reinterpret_cast<u32x2*>(p.out + qrow * p.o_st + head * p.o_sh + gl * 4) =
       u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
   if (p.lse && gl == 0)
@@ -815,7 +860,7 @@ DecodePlan plan_of(const moe_attn_config& c) {
   d.rows = c.q_len * (c.heads_q / c.heads_kv);
   const int rt = row_tiles(d.rows, c.head_dim);
   d.rgroups = (d.rows + 16 * rt - 1) / (16 * rt);
-  d.pieces = std::max(1, (rt == 1 ? kPieces : kPiecesRows) / (c.heads_kv * d.rgroups));
+  d.pieces = std::max(1, (rt == 1 ? kPieces : pieces_rows(c.batch)) / (c.heads_kv * d.rgroups));
   d.slots = (int64_t)d.pieces + c.batch;
   return d;
 }
@@ -858,7 +903,8 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.part_m = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.part_l = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.meta = reinterpret_cast<int2*>(w);
-  const dim3 grid((unsigned)((whole ? c.batch : d.pieces) * c.heads_kv * d.rgroups));
+  const int64_t cut = row_tiles(d.rows, c.head_dim) == 1 ? d.pieces : d.slots;
+  const dim3 grid((unsigned)((whole ? c.batch : cut) * c.heads_kv * d.rgroups));
   const int rt = row_tiles(d.rows, c.head_dim);
   const bool f8 = kv.format == MOE_KV_FP8;
   const bool one = kv.k == kv.v;
