@@ -22,9 +22,9 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_fp4.so")
 
-if not os.path.exists(LIB_PATH):
+if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_PKG, "_attn_binding.so"))):
     raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python block_scaled_fp4_sqrtsoftplus_amd/build.py` "
+        f"{LIB_PATH} (or _attn_binding.so beside it) is missing: build it with `python block_scaled_fp4_sqrtsoftplus_amd/build.py` "
         "(hipcc, gfx950); this package has no non-HIP fallback")
 
 lib = ctypes.CDLL(LIB_PATH)

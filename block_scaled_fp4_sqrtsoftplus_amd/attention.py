@@ -4,14 +4,16 @@ over the cache, and attention over packed prompts.
 
 Rows are bf16 tensors [tokens, heads, head_dim] whose last index is
 contiguous; the other strides are free (multiples of 8 elements), so slices of
-a fused projection's output are taken as they are.
+a fused projection's output are taken as they are.  Tensors are checked, and
+outputs made, by the binding's native half (csrc/attn_binding.cpp).
 """
 
 import ctypes
 
 import torch
 
-from . import _check, _i32, _i64, _ptr, _sz, _vp, lib
+from . import MoeError, _i32, _i64, _ptr, _sz, _vp, lib
+from . import _attn_binding as _native
 
 KV_BF16, KV_FP8 = 0, 1
 
@@ -54,52 +56,14 @@ _byref = ctypes.byref
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream(device):
-    return _raw_stream(device.index)
+_native.set_error(MoeError)
 
 
-_bf16, _int32, _int64 = torch.bfloat16, torch.int32, torch.int64
-
-
-def _refuse(t, dtype, shape, device, name):
-    """Raises for what is wrong with an argument."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError("tensors passed to the HIP library must be on the GPU")
-    raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-
-
-# The checks below run on every call of a decode step, where the host's time
-# is what a small call costs: one test for all that is usual, the reasons apart.
-
-
-def _rows(t, tokens, heads, dim, device, name):
-    """MoeRowsC of a [tokens, heads, dim] bf16 tensor on the GPU `device`."""
-    if t.dtype is not _bf16 or t.shape != (tokens, heads, dim) or t.device != device:
-        _refuse(t, _bf16, (tokens, heads, dim), device, name)
-    st, sh, se = t.stride()
-    if se != 1:
-        raise ValueError(f"{name}: the last index must be contiguous")
-    # strides over indices of one value are free
-    return MoeRowsC(t.data_ptr() or None, st if tokens > 1 else 0, sh if heads > 1 else 0)
-
-
-def _new_rows(tokens, heads, dim, device):
-    """A new [tokens, heads, dim] bf16 tensor and its MoeRowsC."""
-    t = torch.empty((tokens, heads, dim), dtype=_bf16, device=device)
-    return t, MoeRowsC(t.data_ptr() or None, heads * dim, dim)
-
-
-def _ints(t, dtype, shape, device, name):
-    """The address of a contiguous tensor on the GPU `device`."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
-        _refuse(t, dtype, shape, device, name)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or _ptr(t)
+def _bytes_at(t, shape, device, name):
+    """The address of a contiguous uint8 tensor on `device`."""
+    if t.dtype is not torch.uint8 or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be uint8 {tuple(shape)} on {device}")
+    return _ptr(t)
 
 
 class KVCache:
@@ -138,12 +102,12 @@ class KVCache:
             shape = (*k.shape[:3], max(1, self.head_dim // 128))
             if k_scale is None or v_scale is None:
                 raise ValueError("an FP8 cache needs k_scale and v_scale")
-            ks = _ints(k_scale, torch.uint8, shape, self.device, "k_scale")
-            vs = _ints(v_scale, torch.uint8, shape, self.device, "v_scale")
+            ks = _bytes_at(k_scale, shape, self.device, "k_scale")
+            vs = _bytes_at(v_scale, shape, self.device, "v_scale")
         st = k.stride()
         self.c = MoeKvCacheC(k.data_ptr() or None, v.data_ptr() or None, ks, vs, self.pages, st[0], st[1], st[2],
                              self.page_size, self.heads, self.head_dim, self.format)
-        self._ref = _byref(self.c)
+        self._at, self._index = ctypes.addressof(self.c), self.device.index
 
     @classmethod
     def empty(cls, pages, page_size, heads, head_dim, format=KV_BF16, shared=False, device="cuda"):
@@ -169,7 +133,7 @@ class Rope:
             raise ValueError("cos_sin must be float32 [positions, rot_dim]")
         self.cos_sin, self.device = cos_sin, cos_sin.device
         self.c = MoeRopeC(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], rot_offset, int(interleaved), 0)
-        self._ref = _byref(self.c)
+        self._at, self._index = ctypes.addressof(self.c), self.device.index
 
     @classmethod
     def of(cls, positions, rot_dim, base=10000.0, rot_offset=0, interleaved=False, device="cuda"):
@@ -184,31 +148,13 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope: Rope = None, q=
     """Rotate q and k, store k and v at `slots` of the cache (moe_kv_append);
     returns q_out (a new tensor if q is given without one; None without q).
     v is None exactly when the cache has one tensor for keys and values."""
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, heads, head_dim]")
-    tokens, heads, dim, dev = k.shape[0], cache.heads, cache.head_dim, cache.device
-    kc = _rows(k, tokens, heads, dim, dev, "k")
-    vc = _byref(_rows(v, tokens, heads, dim, dev, "v")) if v is not None else None
-    sl = _ints(slots, _int64, (tokens,), dev, "slots")
-    ps = _ints(positions, _int32, (tokens,), dev, "positions") if positions is not None else None
-    if rope is not None and rope.device != dev:
-        raise ValueError("rope is on another device than the cache")
-    qc = oc = None
-    hq = 0
-    if q is not None:
-        hq = q.shape[1]
-        qc = _byref(_rows(q, tokens, hq, dim, dev, "q"))
-        if q_out is None:
-            q_out, oc = _new_rows(tokens, hq, dim, dev)
-        else:
-            oc = _rows(q_out, tokens, hq, dim, dev, "q_out")
-        oc = _byref(oc)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    ko = _byref(_rows(k_out, tokens, heads, dim, dev, "k_out")) if k_out is not None else None
-    _check(lib.moe_kv_append(cache._ref, rope._ref if rope is not None else None, tokens, sl, ps, _byref(kc), vc,
-                             hq, qc, oc, ko, _stream(dev)))
-    return q_out
+    index = cache._index
+    at = 0
+    if rope is not None:
+        if rope._index != index:
+            raise ValueError("rope is on another device than the cache")
+        at = rope._at
+    return _native.kv_append(cache._at, at, index, _raw_stream(index), k, v, slots, positions, q, q_out, k_out)
 
 
 def attn_workspace_size(batch, heads_q, heads_kv, head_dim, q_len=1):
@@ -227,8 +173,8 @@ class DecodeAttention:
         self.tokens = batch * q_len
         scale = cache.head_dim ** -0.5 if scale is None else scale
         self.c = MoeAttnConfigC(self.tokens, 0, batch, q_len, heads_q, cache.heads, cache.head_dim, 1, window, scale)
-        self._ref = _byref(self.c)
-        self.ws_bytes = lib.moe_attn_workspace_size(self._ref)
+        self._at, self._index = ctypes.addressof(self.c), cache._index
+        self.ws_bytes = lib.moe_attn_workspace_size(_byref(self.c))
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=cache.device)
         self._ws = self.ws.data_ptr()
 
@@ -236,21 +182,9 @@ class DecodeAttention:
         """q [batch * q_len, heads_q, head_dim] bf16, block_table [batch, width]
         int32, seq_lens [batch] int32 (new tokens included): out like q, and
         with want_lse also lse [batch * q_len, heads_q] fp32."""
-        cache, n, dev = self.cache, self.tokens, self.cache.device
-        qc = _rows(q, n, self.heads_q, cache.head_dim, dev, "q")
-        if out is None:
-            out, oc = _new_rows(n, self.heads_q, cache.head_dim, dev)
-        else:
-            oc = _rows(out, n, self.heads_q, cache.head_dim, dev, "out")
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [batch, width]")
-        width = block_table.shape[1]
-        bt = _ints(block_table, _int32, (self.batch, width), dev, "block_table")
-        sl = _ints(seq_lens, _int32, (self.batch,), dev, "seq_lens")
-        lse = torch.empty((n, self.heads_q), dtype=torch.float32, device=dev) if want_lse else None
-        _check(lib.moe_attn_decode(self._ref, _byref(qc), cache._ref, bt, width, sl, _byref(oc),
-                                   lse.data_ptr() if want_lse else None, self._ws, self.ws_bytes, _stream(dev)))
-        return (out, lse) if want_lse else out
+        index = self._index
+        return _native.attn_decode(self._at, self.cache._at, index, _raw_stream(index), self._ws, self.ws_bytes, q,
+                                   block_table, seq_lens, out, want_lse)
 
 
 def attn_decode(q, cache: KVCache, block_table, seq_lens, q_len=1, window=0, scale=None, out=None, want_lse=False):
@@ -263,27 +197,7 @@ def attn_prefill(q, k, v, cu_q, cu_k=None, causal=True, window=0, scale=None, ou
     """Attention over packed prompts (moe_attn_prefill): q [tokens, heads_q, head_dim], k and v [tokens_kv, heads_kv,
     head_dim] bf16, cu_q and cu_k [sequences + 1] int32; returns out like q, and with want_lse also lse
     [tokens, heads_q] fp32."""
-    if q.dim() != 3 or k.dim() != 3 or cu_q.dim() != 1:
-        raise ValueError("q, k and v must be [tokens, heads, head_dim], cu_q [sequences + 1]")
     if not q.is_cuda:
         raise ValueError("tensors passed to the HIP library must be on the GPU")
-    (tokens, hq, dim), (keys, hkv, _), dev = q.shape, k.shape, q.device
-    if cu_q.shape[0] < 1:
-        raise ValueError("cu_q has sequences + 1 entries")
-    if cu_k is None and keys != tokens:
-        raise ValueError("without cu_k, k has as many rows as q")
-    qc, kc = _rows(q, tokens, hq, dim, dev, "q"), _rows(k, keys, hkv, dim, dev, "k")
-    vc = kc if v is k else _rows(v, keys, hkv, dim, dev, "v")
-    batch = cu_q.shape[0] - 1
-    cq = _ints(cu_q, _int32, (batch + 1,), dev, "cu_q")
-    ck = _ints(cu_k, _int32, (batch + 1,), dev, "cu_k") if cu_k is not None else None
-    if out is None:
-        out, oc = _new_rows(tokens, hq, dim, dev)
-    else:
-        oc = _rows(out, tokens, hq, dim, dev, "out")
-    lse = torch.empty((tokens, hq), dtype=torch.float32, device=dev) if want_lse else None
-    c = MoeAttnConfigC(tokens, keys, batch, 1, hq, hkv, dim, int(causal), window,
-                       dim ** -0.5 if scale is None else scale)
-    _check(lib.moe_attn_prefill(_byref(c), _byref(qc), _byref(kc), _byref(vc), cq, ck, _byref(oc),
-                                lse.data_ptr() if want_lse else None, _stream(dev)))
-    return (out, lse) if want_lse else out
+    index = q.get_device()
+    return _native.attn_prefill(index, _raw_stream(index), q, k, v, cu_q, cu_k, causal, window, scale, out, want_lse)
