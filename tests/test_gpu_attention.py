@@ -78,6 +78,8 @@ def _table(n, rot):
     (5000, 2, 1, 64, False, 64, 0, False, 16, False),      # more tokens than waves that share a token
     (4100, 1, 1, 128, True, 128, 0, True, 256, False),
     (12, 0, 2, 128, False, 0, 0, False, 16, False),        # no q, no rotation
+    (19000, 24, 2, 64, False, 64, 0, False, 16, False),    # rows read past the caches
+    (19000, 24, 2, 64, True, 32, 32, True, 64, False),
 ])
 def test_kv_append_bits(tokens, hq, hkv, dim, fp8, rot, offset, inter, page, by_token):
     rng = np.random.default_rng(tokens * 7 + dim)
