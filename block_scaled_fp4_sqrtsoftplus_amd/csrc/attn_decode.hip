@@ -704,6 +704,8 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
 
   if (first < last) fetch(0, first);
   put(0);
+#pragma unroll
+  for (int j = 0; j < NF; ++j) arrived(__builtin_bit_cast(u32x4, qf[j]));
   step_barrier<0>();
   int buf = 0;
   for (int key0 = first; key0 < last; key0 += KT, buf ^= 1) {

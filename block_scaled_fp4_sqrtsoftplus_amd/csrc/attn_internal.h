@@ -86,6 +86,14 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Waits here for a value's load.  Before a loop with asynchronous loads: the
+// compiler would otherwise wait at the value's first use inside, each time
+// round, and with it for the loads that it does not know of.
+template <class T>
+__device__ __forceinline__ void arrived(const T& x) {
+  asm volatile("" ::"v"(x));
+}
+
 // The running maximum follows the scores only when one passes it by more than
 // this (base 2): weights then reach 2^kLag, which fp32 sums and bf16's
 // exponent hold as well, and the output is seldom rescaled.

@@ -294,6 +294,10 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   };
 
   const int steps = key_hi > key_lo ? (key_hi - key_lo + BN - 1) / BN : 0;
+  auto q_arrived = [&]() {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) arrived(__builtin_bit_cast(u32x4, qf[j]));
+  };
   u32x4 pw[2 * NK];
   // the weight of element e of the step, in three parts that may be apart
   auto weight_arg = [&](f32x16(&sc)[NK], int e) {
@@ -345,6 +349,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
         if (i < steps) fetch(0, i, key_lo + i * BN);
         if (i < BUFS - 1 && i < steps) fetch(1, i, key_lo + i * BN);
       }
+      q_arrived();
       step_barrier<0>();
       scores(0, sc);
       if constexpr (SPLIT == 2) {
@@ -464,6 +469,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
     f32x16 sc[NK];
     int kb = 0, vb = 0;
     if (steps > 0) fetch(0, 0, key_lo);
+    q_arrived();
     step_barrier<0>();
     auto step = [&](int it, auto first) {
       constexpr bool LAG = !decltype(first)::value;
@@ -516,6 +522,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       fetch(0, 0, key_lo);
       fetch(1, 0, key_lo);
     }
+    q_arrived();
     step_barrier<0>();
     for (int it = 0; it < steps; ++it) {
       const int key0 = key_lo + it * BN;
