@@ -580,6 +580,7 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
   constexpr int NG = D < 128 ? 1 : D / 128;
   constexpr int TB = KT * D * 2;
   constexpr int NT = ONE ? 1 : 2;
+  constexpr int AHEAD = D == 512 && KP == 2 ? 2 : 4;   // registers
   constexpr int LD = C / (2 * RT);            // chunks a thread stages per tensor
   constexpr int JOIN = KP > 1 ? RT * (KP / 2) * (NB * 256 + 128) * 4 : 0;
   constexpr int LDS = 2 * NT * TB > JOIN ? 2 * NT * TB : JOIN;
@@ -723,18 +724,31 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
     int va = (ONE ? 0 : 2 * TB) + buf * TB + kv_at<D>(vr, (col & 3) >> 1) + (col & 1) * 8;
     asm volatile("" : "+v"(ka), "+v"(va));
     if (tile_live && (KP == 1 || mykey < last)) {
+      // LDS reads run AHEAD products before their use, in an order fixed by hand
+      constexpr int QK = 2 * NF;
+      auto read = [&](int i) {
+        if (i < QK) {                         // tile i % 2, columns i / 2
+          const int j = i / 2;
+          return __builtin_bit_cast(
+              bf16x8, *reinterpret_cast<const u32x4*>(lds + (ka ^ ((j & 3) * 64)) +
+                                                      (j >> 2) * 256 + (i % 2) * 16 * D * 2));
+        }
+        const int b = i - QK;
+        const char* v0 = lds + (va ^ ((b & 7) * 32)) + (b >> 3) * 256;
+        return read_tr(v0, v0 + 16 * D * 2);
+      };
+      bf16x8 f[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) f[i] = read(i);
       f32x4 s[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < NF; ++j)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const bf16x8 kf = __builtin_bit_cast(
-              bf16x8, *reinterpret_cast<const u32x4*>(lds + (ka ^ ((j & 3) * 64)) +
-                                                      (j >> 2) * 256 + t * 16 * D * 2));
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[j], s[t], 0, 0, 0);
-        }
+      for (int i = 0; i < QK; ++i) {
+        s[i % 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[i % AHEAD], qf[i / 2], s[i % 2], 0, 0, 0);
+        f[i % AHEAD] = read(i + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       float pr[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) pr[i] = s[i >> 2][i & 3] * p.scale2;
@@ -765,9 +779,9 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
       const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const char* v0 = lds + (va ^ ((b & 7) * 32)) + (b >> 3) * 256;
-        const bf16x8 vf = read_tr(v0, v0 + 16 * D * 2);
-        o[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, o[b], 0, 0, 0);
+        o[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[(QK + b) % AHEAD], pf, o[b], 0, 0, 0);
+        if (b + AHEAD < NB) f[(QK + b) % AHEAD] = read(QK + b + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (more) put(buf ^ 1);
