@@ -166,7 +166,8 @@ def attn_workspace_size(batch, heads_q, heads_kv, head_dim, q_len=1):
 class DecodeAttention:
     """Holds the sizes, the cache and the workspace of moe_attn_decode and runs
     it on the current stream: attention of every sequence's newest q_len tokens
-    over the cache, which holds them already."""
+    over the cache, which holds them already.  Calls that may overlap, on other
+    streams, need an object each: they would share the workspace."""
 
     def __init__(self, cache: KVCache, batch, heads_q, q_len=1, window=0, scale=None):
         self.cache, self.batch, self.heads_q, self.q_len = cache, batch, heads_q, q_len

@@ -9,9 +9,11 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "moe_attn.h"
@@ -78,6 +80,12 @@ void* ints(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, int 
   return base ? base + t.storage_offset() * t.element_size() : nullptr;
 }
 
+// The tensors' GPU is the current one for a call.
+struct OnDevice {
+  c10::DeviceGuard guard;
+  explicit OnDevice(int index) : guard(at::Device(at::kCUDA, (c10::DeviceIndex)index)) {}
+};
+
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, index)));
 }
@@ -135,6 +143,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* rope = address<const moe_rope>(a[1]);
   const int index = (int)number(a[2]);
   void* stream = address<void>(a[3]);
+  const OnDevice on(index);
   const int64_t heads = cache->heads, dim = cache->head_dim;
   const at::Tensor& kt = tensor(a[4], "k");
   const moe_rows k = rows(kt, -1, heads, dim, index, "k");
@@ -183,6 +192,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* cache = address<const moe_kv_cache>(a[1]);
   const int index = (int)number(a[2]);
   void* stream = address<void>(a[3]);
+  const OnDevice on(index);
   const int64_t tokens = cfg->tokens, hq = cfg->heads_q, dim = cfg->head_dim, batch = cfg->batch;
   const moe_rows q = rows(tensor(a[6], "q"), tokens, hq, dim, index, "q");
   const at::Tensor& tt = tensor(a[7], "block_table");
@@ -212,6 +222,7 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!expects(n, 12)) return nullptr;
   const int index = (int)number(a[0]);
   void* stream = address<void>(a[1]);
+  const OnDevice on(index);
   const at::Tensor &qt = tensor(a[2], "q"), &kt = tensor(a[3], "k"), &vt = tensor(a[4], "v");
   const at::Tensor& cu = tensor(a[5], "cu_q");
   if (qt.dim() != 3 || kt.dim() != 3 || cu.dim() != 1)

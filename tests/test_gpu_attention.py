@@ -387,6 +387,52 @@ def test_attn_prefill_offsets_out_of_range_stay_in_bounds():
 
 
 # ----------------------------------------------------------------------------
+# Offsets past 32 bits
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("fp8,hq,dim", [(False, 8, 128), (True, 8, 128), (False, 40, 128)])
+def test_far_pages_of_a_large_cache(fp8, hq, dim):
+    # 4.9 GiB (bf16) or 2.4 GiB (FP8, past 2^31 bytes); the sequence's pages are the last ones
+    rng = np.random.default_rng(50 + hq)
+    hkv, page, n = 2, 64, 150
+    pages = int((5.2e9 if not fp8 else 2.6e9) / (hkv * page * dim * (1 if fp8 else 2)))
+    cache = moe.KVCache.empty(pages, page, hkv, dim, moe.KV_FP8 if fp8 else moe.KV_BF16, shared=True)
+    table = np.array([[pages - 1, pages - 3, pages - 2]], np.int32)
+    at = np.arange(n)
+    slots = table[0, at // page].astype(np.int64) * page + at % page
+    k, q = _vals(rng, n, hkv, dim), _vals(rng, 1, hq, dim)
+    moe.kv_append(cache, dev_bf16(k), None, dev(slots))
+    out, lse = moe.attn_decode(dev_bf16(q), cache, dev(table), dev(np.array([n], np.int32)), want_lse=True)
+    torch.cuda.synchronize()
+    rows = _f(k)
+    if fp8:
+        rows = attention.fp8_values(*_quant_rows(rows))
+    rows = rows.swapaxes(0, 1)
+    _check(out, lse, attention.attend(_f(q), rows, rows, n - 1, dim ** -0.5), dim)
+    del cache
+    torch.cuda.empty_cache()
+
+
+def test_prefill_rows_far_apart():
+    # a token stride of 2^22 elements: the last rows lie past 2^32 bytes
+    rng = np.random.default_rng(60)
+    n, dim, step = 600, 64, 1 << 22
+    q, k = _vals(rng, n, 2, dim), _vals(rng, n, 1, dim)
+    wide = torch.zeros(n * step, dtype=torch.bfloat16, device="cuda").view(n, step)
+    wide[:, :2 * dim] = dev_bf16(q).view(n, -1)
+    wide[:, 1024:1024 + dim] = dev_bf16(k).view(n, -1)
+    qd = wide[:, :2 * dim].unflatten(1, (2, dim))
+    kd = wide[:, 1024:1024 + dim].unflatten(1, (1, dim))
+    out, lse = moe.attn_prefill(qd, kd, kd, dev(_cu([n])), want_lse=True)
+    torch.cuda.synchronize()
+    rows = _f(k).swapaxes(0, 1)
+    _check(out, lse, attention.attend(_f(q), rows, rows, 0, dim ** -0.5), dim)
+    del wide, qd, kd
+    torch.cuda.empty_cache()
+
+
+# ----------------------------------------------------------------------------
 # Streams, graphs, refusals
 # ----------------------------------------------------------------------------
 
