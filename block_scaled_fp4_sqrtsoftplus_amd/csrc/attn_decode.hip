@@ -867,10 +867,17 @@ struct DecodePlan {
   int rows, rgroups, pieces;
   int64_t slots;
 };
-// Sequences of no more keys than this are not cut: a workgroup takes
-// one in at most 4 steps, and the call is one kernel (one sequence of 300
-// keys: 10.3 us a call, with a cut and its join 14.5, mostly the second launch).
-constexpr int64_t kWholeKeys = 512;
+// Whether no sequence is cut: a workgroup takes one whole, and the call is one
+// kernel.  A cut costs a second launch and the join; without it a workgroup
+// reads a sequence's keys and values of a head (`bytes` at most) at the rate of one CU.
+// Measured, whole and cut: 300 keys of 128 elements 7.8 and 9.8 us, 8
+// sequences of 450 11.6 and 10.7, 500 keys of 256 elements 17.9 and 13.9; with
+// a workgroup for every CU, 32 sequences of 500 keys 14.3 and 18.9, of 1000
+// 21.3 and 23.4; 4 of 500 in the many-row kernel 42.6 and 19.1.
+bool whole_sequences(int64_t bytes, int64_t workgroups, bool many_rows) {
+  const int64_t most = workgroups >= 256 ? 512 : many_rows ? 128 : 192;
+  return bytes <= most * 1024;
+}
 DecodePlan plan_of(const moe_attn_config& c) {
   DecodePlan d;
   d.rows = c.q_len * (c.heads_q / c.heads_kv);
@@ -909,7 +916,10 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.batch = c.batch; a.q_len = c.q_len; a.hq = c.heads_q; a.hkv = c.heads_kv;
   a.group = c.heads_q / c.heads_kv;
   a.rows = d.rows; a.rgroups = d.rgroups;
-  const bool whole = ((int64_t)table_width << a.page_shift) <= kWholeKeys;
+  const bool one = kv.k == kv.v;
+  const bool whole = whole_sequences(
+      ((int64_t)table_width << a.page_shift) * c.head_dim * eb * (one ? 1 : 2),
+      (int64_t)c.batch * c.heads_kv * d.rgroups, row_tiles(d.rows, c.head_dim) > 1);
   a.pieces = whole ? 0 : d.pieces;
   a.tile_shift = row_tiles(d.rows, c.head_dim) == 1 ? 7 : 6;
   a.window = c.window; a.scale2 = c.scale * kLog2e;
@@ -923,7 +933,6 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   const dim3 grid((unsigned)((whole ? c.batch : cut) * c.heads_kv * d.rgroups));
   const int rt = row_tiles(d.rows, c.head_dim);
   const bool f8 = kv.format == MOE_KV_FP8;
-  const bool one = kv.k == kv.v;
 #define MOE_ROWS(D, F, R, KP, O)                                                              \
   hipLaunchKernelGGL((attn_decode_rows_kernel<D, F, R, KP, O>), grid, dim3(64 * R * KP), 0, st, a)
 #define MOE_ROWS_ANY(D, F, R)                                                                 \

@@ -43,7 +43,7 @@ struct PrefillArgs {
 };
 
 struct Seq {
-  int b, q0, qn, k0, kn, tile;
+  int q0, qn, k0, kn, tile;
 };
 
 __device__ __forceinline__ int clamped(const int32_t* cu, int i, int64_t most) {
@@ -58,11 +58,13 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& p, int tile, Seq& s
   int base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 64) {
     const int b = b0 + lane;
-    int n = 0;
+    int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;   // a sequence per lane
     if (b < p.batch) {
-      const int64_t rows =
-          (int64_t)max(clamped(p.cu_q, b + 1, p.tokens) - clamped(p.cu_q, b, p.tokens), 0) *
-          p.group;
+      q0 = clamped(p.cu_q, b, p.tokens);
+      q1 = clamped(p.cu_q, b + 1, p.tokens);
+      k0 = clamped(p.cu_k, b, p.tokens_kv);
+      k1 = clamped(p.cu_k, b + 1, p.tokens_kv);
+      const int64_t rows = (int64_t)max(q1 - q0, 0) * p.group;
       n = (int)((rows + BM - 1) / BM);
     }
     const int incl = wave_scan(n);
@@ -71,12 +73,11 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& p, int tile, Seq& s
       const int l = __builtin_ctzll(past);
       const int tiles = __builtin_amdgcn_readlane(n, l);
       const int t0 = base + __builtin_amdgcn_readlane(incl, l) - tiles;
-      s.b = __builtin_amdgcn_readfirstlane(b0 + l);
       s.tile = tiles - 1 - (tile - t0);
-      s.q0 = clamped(p.cu_q, s.b, p.tokens);
-      s.qn = clamped(p.cu_q, s.b + 1, p.tokens) - s.q0;
-      s.k0 = clamped(p.cu_k, s.b, p.tokens_kv);
-      s.kn = max(clamped(p.cu_k, s.b + 1, p.tokens_kv) - s.k0, 0);
+      s.q0 = __builtin_amdgcn_readlane(q0, l);
+      s.qn = __builtin_amdgcn_readlane(q1, l) - s.q0;
+      s.k0 = __builtin_amdgcn_readlane(k0, l);
+      s.kn = max(__builtin_amdgcn_readlane(k1, l) - s.k0, 0);
       return true;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
