@@ -86,6 +86,11 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The waves' LDS writes are seen by all; asynchronous loads stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Waits here for a value's load.  Before a loop with asynchronous loads: the
 // compiler would otherwise wait at the value's first use inside, each time
 // round, and with it for the loads that it does not know of.

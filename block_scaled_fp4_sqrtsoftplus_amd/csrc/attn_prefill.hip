@@ -131,6 +131,14 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   const int wave = wv / SPLIT, part = wv % SPLIT;   // row group, slice of the columns
   const int col = lane & 31, hh = lane >> 5;
 
+  // 512-element heads work what depends on the lane out anew each time, from the one
+  // register that holds it
+  auto here = [&]() {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+
   // workgroups go to the 8 XCDs in turn: a key-value head stays on one XCD
   int h, tile;
   {
@@ -150,11 +158,9 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   // this lane's row, and the keys it keeps: [row_lo, row_hi)
   const int64_t rows = (int64_t)s.qn * p.group;
   const int64_t row0 = (int64_t)s.tile * BM;
-  const int64_t row = row0 + wave * 32 + col;
-  const bool live = row < rows;
-  const int tok = (int)(min(row, rows - 1) / p.group);
-  const int head = h * p.group + (int)(min(row, rows - 1) - (int64_t)tok * p.group);
-  const int end = s.kn - s.qn + tok + 1;
+  const int64_t my_row = min(row0 + wave * 32 + col, rows - 1);
+  const int my_tok = (int)(my_row / p.group);
+  const int end = s.kn - s.qn + my_tok + 1;
   const int row_hi = p.causal ? max(min(end, s.kn), 0) : s.kn;
   const int row_lo = p.window > 0 ? max(end - p.window, 0) : 0;
   // the same over the workgroup's rows and over the wave's
@@ -169,7 +175,8 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
 
   bf16x8 qf[NF];
   {
-    const uint16_t* qp = p.q + (s.q0 + tok) * p.q_st + head * p.q_sh;
+    const int head = h * p.group + (int)(my_row - (int64_t)my_tok * p.group);
+    const uint16_t* qp = p.q + (s.q0 + my_tok) * p.q_st + head * p.q_sh;
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       u32x4 w = *reinterpret_cast<const u32x4*>(qp + 16 * (part * NF + j) + 8 * hh);
@@ -192,10 +199,10 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   const char* kb = reinterpret_cast<const char*>(p.k + s.k0 * p.k_st + h * p.k_sh);
   const char* vb = reinterpret_cast<const char*>(p.v + s.k0 * p.v_st + h * p.v_sh);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-  int r0 = tid / C, c0 = tid % C;
+  const int r0 = D == 512 ? wv : tid / C;
   // chunk i of a tile whose rows are all keys
   auto fetch_one = [&](int which, int buf, int key0, int i) {
-    if constexpr (D == 512) asm volatile("" : "+v"(r0), "+v"(c0));   // no places kept over the loop
+    const int c0 = D == 512 ? here() : tid % C;
     const int64_t st = 2 * (which ? p.v_st : p.k_st);
     const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
     load_lds16(lds0 + (which ? V0 : 0) + buf * TB + wv * 1024 + i * TH * 16,
@@ -211,6 +218,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
     } else {
 #pragma unroll 1
       for (int i = 0; i < LD; ++i) {
+        const int c0 = D == 512 ? here() : tid % C;
         const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
         load_lds16(to + i * TH * 16, base + key0 * st,
                    (uint32_t)(min(r0 + RS * i, s.kn - 1 - key0) * (int)st + 16 * c));
@@ -221,9 +229,19 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   // so the other chunks' places are these with some bits flipped.  For large
   // heads they are worked out anew in each step: kept over the loop they would
   // take registers that it does not have.
-  const int k_lane = k_at<D>(col, hh);
-  const int v_lane = v_at<D>(4 * hh + ((lane & 15) >> 2), ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) +
+  const int k_once = k_at<D>(col, hh);
+  const int v_once = v_at<D>(4 * hh + ((lane & 15) >> 2), ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) +
                      (lane & 1) * 8;
+  auto k_lane = [&]() {
+    if constexpr (D < 512) return k_once;
+    const int l = here();
+    return k_at<D>(l & 31, l >> 5);
+  };
+  auto v_lane = [&]() {
+    if constexpr (D < 512) return v_once;
+    const int l = here();
+    return v_at<D>(4 * (l >> 5) + ((l & 15) >> 2), ((l >> 4) & 1) * 2 + ((l & 3) >> 1)) + (l & 1) * 8;
+  };
   constexpr int QK = NK * NF, PV = 2 * NK * ND, NE = 16 * NK;
   auto read_k = [&](int ka, int i) {   // operand of QK product i: tile i % NK, columns i / NK
     const int t = i % NK, c = 2 * (i / NK);   // chunk 2 (part NF + ..) + hh of row 32 t + col
@@ -239,21 +257,22 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   };
   float* xs = reinterpret_cast<float*>(lds + X0);
   auto hand_over = [&](const f32x16(&sc)[NK]) {   // SPLIT 2: this wave's part for the other
+    const int l = here();
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<f32x4*>(xs + ((wv * NK + t) * 4 + i / 4) * 256 + lane * 4) =
+        *reinterpret_cast<f32x4*>(xs + ((wv * NK + t) * 4 + i / 4) * 256 + l * 4) =
             f32x4{sc[t][i], sc[t][i + 1], sc[t][i + 2], sc[t][i + 3]};
   };
   auto take_over = [&](f32x16(&sc)[NK]) {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
+    const int l = here();
 #pragma unroll
     for (int t = 0; t < NK; ++t)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const f32x4 y =
-            *reinterpret_cast<const f32x4*>(xs + (((wv ^ 1) * NK + t) * 4 + i / 4) * 256 + lane * 4);
+            *reinterpret_cast<const f32x4*>(xs + (((wv ^ 1) * NK + t) * 4 + i / 4) * 256 + l * 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[t][i + e] += y[e];
       }
@@ -261,7 +280,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   // whether every row of the wave keeps all of a step's keys; if not, the mask
   auto inner = [&](int key0) { return key0 >= all_lo && key0 + BN <= all_hi; };
   auto mask = [&](int key0, f32x16(&sc)[NK]) {
-    int first = key0 + 4 * hh;
+    int first = key0 + 4 * (here() >> 5);
     asm volatile("" : "+v"(first));    // its places are not kept over the loop
 #pragma unroll
     for (int t = 0; t < NK; ++t)
@@ -322,7 +341,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
     weight_sum(sc, e);
   };
   auto scores = [&](int buf, f32x16(&to)[NK]) {
-    int ka = buf * TB + k_lane;
+    int ka = buf * TB + k_lane();
     if constexpr (D >= 256) asm volatile("" : "+v"(ka));
 #pragma unroll
     for (int t = 0; t < NK; ++t)
@@ -333,7 +352,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       to[i % NK] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_k(ka, i), qf[i / NK], to[i % NK], 0, 0, 0);
   };
   auto values = [&](int buf) {
-    int va = V0 + buf * TB + v_lane;
+    int va = V0 + buf * TB + v_lane();
     if constexpr (D >= 256) asm volatile("" : "+v"(va));
 #pragma unroll
     for (int i = 0; i < PV; ++i)
@@ -353,10 +372,6 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       q_arrived();
       step_barrier<0>();
       scores(0, sc);
-      if constexpr (SPLIT == 2) {
-        hand_over(sc);
-        take_over(sc);
-      }
       if (!inner(key_lo)) mask(key_lo, sc);
       raise(largest(sc));
       step_barrier<0>();
@@ -378,7 +393,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       // One stream of matrix instructions in an order fixed by hand: the QK
       // products of the next step, the weights of this one dealt out
       // behind them, then the PV products.
-      int ka = kb_next * TB + k_lane, va = V0 + vb_now * TB + v_lane;
+      int ka = kb_next * TB + k_lane(), va = V0 + vb_now * TB + v_lane();
       asm volatile("" : "+v"(ka), "+v"(va));
       auto read = [&](int i) { return i < QK ? read_k(ka, i) : read_v(va, i - QK); };
       // the elements behind product i
@@ -412,7 +427,6 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       }
 #pragma unroll
       for (int e = from(QK - 1); e < NE; ++e) weight_exp(sc, e);
-      if constexpr (SPLIT == 2) hand_over(nx);
       float mx[4];
 #pragma unroll
       for (int i = 0; i < PV; ++i) {
@@ -423,15 +437,14 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
 #pragma unroll
           for (int e = from(QK - 2 + i); e < from(QK - 1 + i); ++e) weight_sum(sc, e);
         }
-        if constexpr (WHOLE && SPLIT == 1) {
+        if constexpr (WHOLE) {
 #pragma unroll
           for (int e = i * NE / PV; e < (i + 1) * NE / PV; ++e)
             mx[e % 4] = e < 4 ? nx[e / 16][e % 16] : fmaxf(mx[e % 4], nx[e / 16][e % 16]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (SPLIT == 2) take_over(nx);
-      if constexpr (WHOLE && SPLIT == 1) {
+      if constexpr (WHOLE) {
         raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
       } else {
         if (!WHOLE && !inner(key0 + BN)) mask(key0 + BN, nx);
@@ -464,22 +477,20 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
       values(vb_now);
     }
   } else if constexpr (SPLIT == 2) {
-    // The product with V lags a step behind, so that it runs while the waves'
-    // parts of S pass through LDS.  Tiles of K take turns in kb, kb_next .., the
-    // lagging tile of V is vb; with ONE that is K's of the step before.
+    // Half of a step is matrix products (its scores, and with V of the step
+    // before), half vector instructions (the other wave's part of the scores,
+    // the weights).  The second four waves, which share the SIMDs of the first, are half
+    // a step late, so that products run beside weights: 335 us instead of 350 at
+    // 2048 tokens of 64 heads on one.  Tiles of K take turns in kb, kb_next
+    // .., the tile of V is vb; with ONE that is K's of the step before.
     f32x16 sc[NK];
-    int kb = 0, vb = 0;
+    int kb = 0, vb = 0;   // tiles of K and V that are read
     if (steps > 0) fetch(0, 0, key_lo);
     q_arrived();
     step_barrier<0>();
-    auto step = [&](int it, auto first) {
+    auto products = [&](auto first) __attribute__((always_inline)) {
       constexpr bool LAG = !decltype(first)::value;
-      const int key0 = key_lo + it * BN;
-      const int kb_next = kb + 1 == (ONE ? 3 : 2) ? 0 : kb + 1;
-      const int vb_next = ONE ? kb : vb ^ 1;
-      if (it + 1 < steps) fetch(0, kb_next, key0 + BN);
-      if constexpr (!ONE) fetch(1, vb_next, key0);
-      int ka = kb * TB + k_lane, va = V0 + vb * TB + v_lane;
+      int ka = kb * TB + k_lane(), va = V0 + vb * TB + v_lane();
       asm volatile("" : "+v"(ka), "+v"(va));
       auto read = [&](int i) { return i < QK ? read_k(ka, i) : read_v(va, i - QK); };
       constexpr int N = LAG ? QK + PV : QK;
@@ -504,18 +515,41 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
         if (i + AHEAD < N) f[i % AHEAD] = read(i + AHEAD);
         __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    auto weights = [&](int key0) __attribute__((always_inline)) {
       take_over(sc);
       if (!inner(key0)) mask(key0, sc);
       raise(largest(sc));
 #pragma unroll
       for (int e = 0; e < NE; ++e) weight(sc, e);
+    };
+    // one step of early or late waves: both pass the same two barriers
+    auto step = [&](int it, auto first, auto late) __attribute__((always_inline)) {
+      constexpr bool LATE = decltype(late)::value;
+      const int key0 = key_lo + it * BN;
+      const int kb_next = kb + 1 == (ONE ? 3 : 2) ? 0 : kb + 1;
+      const int vb_next = ONE ? kb : vb ^ 1;
+      if (it + 1 < steps) fetch(0, kb_next, key0 + BN);
+      if constexpr (!ONE) fetch(1, vb_next, key0);
+      if constexpr (!LATE) products(first);
+      else if constexpr (!decltype(first)::value) weights(key0 - BN);
+      lds_barrier();
+      if constexpr (LATE) products(first); else weights(key0);
       kb = kb_next;
       vb = vb_next;
       step_barrier<0>();
     };
+    auto walk = [&](auto late) __attribute__((always_inline)) {
+      step(0, std::true_type{}, late);
+      for (int it = 1; it < steps; ++it) step(it, std::false_type{}, late);
+    };
     if (steps > 0) {
-      step(0, std::true_type{});
-      for (int it = 1; it < steps; ++it) step(it, std::false_type{});
+      if (wv < 4) {
+        walk(std::false_type{});
+      } else {
+        walk(std::true_type{});
+        weights(key_lo + (steps - 1) * BN);
+      }
       values(vb);
     }
   } else {
@@ -545,18 +579,30 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
 
   l += l2;
   l += __shfl_xor(l, 32);
-  if (!live) return;
+  // the row again, so that the loop need not hold it
+  const int ln = here();
+  const int64_t row = row0 + wave * 32 + (ln & 31);
+  if (row >= rows) return;
+  const int tok = (int)(row / p.group);
+  const int head = h * p.group + (int)(row - (int64_t)tok * p.group);
   const float inv = l > 0.f ? 1.0f / l : 0.f;
   uint16_t* dst = p.out + (s.q0 + tok) * p.o_st + head * p.o_sh;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const u32x2 w = {pack_bf16(o[d][i] * inv, o[d][i + 1] * inv),
-                       pack_bf16(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-      *reinterpret_cast<u32x2*>(dst + 32 * (part * ND + d) + 2 * i + 4 * hh) = w;
+    for (int i = 0; i < 16; i += 8) {
+      // 4 columns of two eighths each: the row's other lane takes the second
+      // eighth's for the first one's, so that each stores one of 16 bytes
+      const u32x2 x = __builtin_amdgcn_permlane32_swap(pack_bf16(o[d][i] * inv, o[d][i + 1] * inv),
+                                                       pack_bf16(o[d][i + 4] * inv, o[d][i + 5] * inv),
+                                                       false, false);
+      const u32x2 y = __builtin_amdgcn_permlane32_swap(pack_bf16(o[d][i + 2] * inv, o[d][i + 3] * inv),
+                                                       pack_bf16(o[d][i + 6] * inv, o[d][i + 7] * inv),
+                                                       false, false);
+      *reinterpret_cast<u32x4*>(dst + 32 * (part * ND + d) + 2 * i + 8 * (ln >> 5)) =
+          u32x4{x[0], y[0], x[1], y[1]};
     }
-  if (p.lse && hh == 0 && part == 0)
+  if (p.lse && ln < 32 && part == 0)
     p.lse[(int64_t)(s.q0 + tok) * p.hq + head] =
         l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
