@@ -19,7 +19,16 @@
 // to registers without LDS: K's operand is 16 bytes of one key per lane; V's
 // needs 8 keys of one column per lane, which a lane gets by loading the same 8
 // columns of its 8 keys (a wave then covers whole rows) and transposing 8 x 8
-// in registers.
+// in registers.  P is rounded to bf16 as v is: kept as the sum of two bf16
+// values (16 bits) the output is nearer to the exact one by less than its own
+// rounding (1.7e-3 instead of 2.3e-3 in the 2-norm), for 1 to 13% of the time.
+//
+// Bound by the reads of K and V, each row once.  Measured: 64 sequences of up to
+// 4096 keys, 8 heads of 128 in bf16 106 us (6.1 TB/s; the join kernel takes 4.5 of
+// them); one sequence of 131071 keys in FP8 49 us (5.5 TB/s); 32 sequences of up to 4096
+// keys, 64 query heads on one 512-element head that is keys and values 46 us
+// (2.2 TB/s: 35 and a join of 7.6, with 31 MB of partial results between
+// them); 300 keys of 8 heads 7.8 us, a chain of latencies.
 #include <algorithm>
 
 #include "attn_internal.h"
@@ -30,10 +39,10 @@ namespace {
 
 // Pieces the work is cut into: two workgroups a CU for the kernel without LDS
 // (of 256, 512, 768 and 1024 pieces the best or within 1% of it for 64 ragged
-// sequences, one long one and 256-element heads).  The one with LDS has one
+// sequences, one long one and 256-element heads; 1024 take 3% and 10% more on the first two).  The one with LDS has one
 // workgroup a CU, and its own cut adds up to a piece per sequence: together
-// they stay below the CUs, since a second round doubles the time (85 instead
-// of 60 us at 32 sequences on one 512-element head).
+// they stay below the CUs, since the kernel has a second round otherwise (69 instead
+// of 48 us at 32 sequences on one 512-element head).
 constexpr int kPieces = 512;
 int pieces_rows(int batch) { return std::max(256 - batch, 128); }
 
@@ -574,6 +583,10 @@ __device__ __forceinline__ int kv_at(int r, int c) {
 // step each.  A step's tiles are loaded while the one before is computed:
 // bf16 straight into LDS, FP8 through registers, turned into bf16 once for all waves.
 // ONE: one tensor serves as keys and values, and is loaded once.
+// At 32 sequences of up to 4096 keys with 64 rows on one 512-element head: 35 us, of
+// which a workgroup's start (its piece, q, the first tiles) takes 7, eight steps
+// of 64 KB 23 (5 TB/s over all CUs) and its partial result 5.  32 rows a workgroup and twice the
+// steps write half as many partial results, but take 10 us more.
 template <int D, bool FP8, int RT, int KP, bool ONE>
 __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_decode_rows_kernel(
     DecodeArgs p) {
@@ -863,9 +876,16 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
     p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
 }
 
-// Row tiles of a workgroup; 1: the kernel without LDS.  512-element heads have
-// no registers for that one, and no LDS for the twofold step of two tiles.
-int row_tiles(int rows, int dim) { return dim == 512 ? 4 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Row tiles of a workgroup; 1: the kernel without LDS, which for up to 16 rows
+// takes 107 us where the other takes 132 (64 sequences of up to 4096 keys, 4 rows
+// of 128 elements a head), with FP8 51 and 116 (one of 131071).  512-element heads have no registers for it.
+// Two tiles for 17 to 32 rows, and twice as many keys a step: 64 us instead of
+// 77 with four (32 sequences of 4096 keys, 32 rows of 128 elements); with 256
+// elements four, since a twofold step takes most of the LDS and leaves one
+// workgroup on a CU (16 sequences of 4096: 70 us with two, 62 with four).
+int row_tiles(int rows, int dim) {
+  return dim == 512 ? 4 : rows <= 16 ? 1 : rows <= 32 && dim < 256 ? 2 : 4;
+}
 
 struct DecodePlan {
   int rows, rgroups, pieces;
@@ -874,10 +894,10 @@ struct DecodePlan {
 // Whether no sequence is cut: a workgroup takes one whole, and the call is one
 // kernel.  A cut costs a second launch and the join; without it a workgroup
 // reads a sequence's keys and values of a head (`bytes` at most) at the rate of one CU.
-// Measured, whole and cut: 300 keys of 128 elements 7.8 and 9.8 us, 8
-// sequences of 450 11.6 and 10.7, 500 keys of 256 elements 17.9 and 13.9; with
-// a workgroup for every CU, 32 sequences of 500 keys 14.3 and 18.9, of 1000
-// 21.3 and 23.4; 4 of 500 in the many-row kernel 42.6 and 19.1.
+// Measured, whole and cut: 300 keys of 128 elements 7.8 and 9.7 us, 8
+// sequences of 450 11.6 and 10.7, 500 keys of 256 elements 17.8 and 14.0; with
+// a workgroup for every CU, 32 sequences of 500 keys 14.5 and 18.9, of 1000
+// 21.4 and 23.2; in the many-row kernel 3 of 120 16.9 and 18.8, 4 of 500 39 and 19.
 bool whole_sequences(int64_t bytes, int64_t workgroups, bool many_rows) {
   const int64_t most = workgroups >= 256 ? 512 : many_rows ? 128 : 192;
   return bytes <= most * 1024;
@@ -944,9 +964,11 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
     if (one) MOE_ROWS(D, F, R, (D == 512 ? 2 : 4 / R), true);                                 \
     else MOE_ROWS(D, F, R, 4 / R, false);                                                     \
   } while (0)
+#define MOE_DIRECT(D, F)                                                                      \
+  hipLaunchKernelGGL((attn_decode_kernel<D, F>), grid, dim3(256), 0, st, a)
 #define MOE_FEW(D, F)                                                                         \
   do {                                                                                        \
-    if (rt == 1) hipLaunchKernelGGL((attn_decode_kernel<D, F>), grid, dim3(256), 0, st, a);   \
+    if (rt == 1) MOE_DIRECT(D, F);                                                            \
     else if (rt == 2) MOE_ROWS_ANY(D, F, 2);                                                  \
     else MOE_ROWS_ANY(D, F, 4);                                                               \
   } while (0)
@@ -955,7 +977,14 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
     if (f8) MOE_FEW(D, true); else MOE_FEW(D, false);                                         \
     break;
   switch (c.head_dim) {
-    MOE_DECODE(64) MOE_DECODE(128) MOE_DECODE(256)
+    MOE_DECODE(64) MOE_DECODE(128)
+    case 256:
+      if (rt == 1) {
+        if (f8) MOE_DIRECT(256, true); else MOE_DIRECT(256, false);
+        break;
+      }
+      if (f8) MOE_ROWS_ANY(256, true, 4); else MOE_ROWS_ANY(256, false, 4);
+      break;
     case 512:
       if (f8) MOE_ROWS_ANY(512, true, 4); else MOE_ROWS_ANY(512, false, 4);
       break;
@@ -963,6 +992,7 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   }
 #undef MOE_DECODE
 #undef MOE_FEW
+#undef MOE_DIRECT
 #undef MOE_ROWS_ANY
 #undef MOE_ROWS
   hipError_t e = hipGetLastError();
