@@ -271,6 +271,36 @@ def test_attn_decode_splits(lens, hq, hkv, dim, fp8):
     assert torch.equal(out, again)             # equal calls give equal bits
 
 
+@pytest.mark.parametrize("hq,hkv,dim,q_len,fp8,shared", [
+    (24, 1, 256, 1, False, False),     # 17 to 32 rows of 256 elements: four row tiles
+    (16, 2, 256, 3, True, False),
+    (12, 1, 256, 2, False, True),
+    (40, 1, 256, 1, True, True),
+])
+def test_attn_decode_rows_of_large_heads(hq, hkv, dim, q_len, fp8, shared):
+    rng = np.random.default_rng(hq + q_len)
+    p = _Paged(rng, LENS, hkv, dim, 32, fp8, shared)
+    q = _vals(rng, len(LENS) * q_len, hq, dim)
+    out, lse = moe.attn_decode(dev_bf16(q), p.cache, dev(p.table), dev(p.lens), q_len, want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, p.reference(q, q_len, dim ** -0.5), dim)
+
+
+@pytest.mark.parametrize("hq,dim", [(8, 128), (24, 128), (40, 256), (64, 512)])
+def test_attn_decode_one_tensor_with_two_sets_of_scales(hq, dim):
+    # keys and values of the same codes, the values four times as large
+    rng = np.random.default_rng(hq)
+    p = _Paged(rng, [400, 33, 0], 1, dim, 16, fp8=True, shared=True)
+    scales = p.cache.k_scale.clone()
+    scales[scales != 255] += 2
+    p.cache.c.v_scale = scales.data_ptr()
+    p.v = p.v * 4
+    q = _vals(rng, 3, hq, dim)
+    out, lse = moe.attn_decode(dev_bf16(q), p.cache, dev(p.table), dev(p.lens), want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, p.reference(q, 1, dim ** -0.5), dim)
+
+
 def test_attn_decode_window_leaves_freed_pages_unread():
     # pages before every row's window are gone from the table
     rng = np.random.default_rng(9)
