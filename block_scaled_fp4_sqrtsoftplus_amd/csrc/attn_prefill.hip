@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   const int wtok_z = (int)(min(row0 + wave * 32 + 31, rows - 1) / p.group);
   auto hi_of = [&](int t) { return p.causal ? max(min(s.kn - s.qn + t + 1, s.kn), 0) : s.kn; };
   auto lo_of = [&](int t) { return p.window > 0 ? max(s.kn - s.qn + t + 1 - p.window, 0) : 0; };
-  const int key_lo = lo_of(tok_a) / BN * BN, key_hi = hi_of(tok_z);
+  const int key_first = lo_of(tok_a), key_lo = key_first / BN * BN, key_hi = hi_of(tok_z);
   const int all_lo = lo_of(wtok_z), all_hi = hi_of(wtok_a);   // kept by every row of the wave
 
   bf16x8 qf[NF];
@@ -201,8 +201,10 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
 
   // Staging: chunk i of a thread is chunk tid + TH i of the tile, in row
   // r0 + RS i.  Its place in the row is permuted on the global side, since the
-  // load writes LDS in lane order.  Rows past the last key repeat it (their
-  // weights are zero, and the row is finite).
+  // load writes LDS in lane order.  Rows past the last key repeat it, and rows
+  // before the first key that the workgroup's rows keep repeat that one: their weights are
+  // zero, but 0 * NaN is not, and the keys repeated are finite while what
+  // lies outside every window may hold anything.
   constexpr int RS = TH / C;
   const char* kb = reinterpret_cast<const char*>(p.k + s.k0 * p.k_st + h * p.k_sh);
   const char* vb = reinterpret_cast<const char*>(p.v + s.k0 * p.v_st + h * p.v_sh);
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
     const char* base = which ? vb : kb;
     const int64_t st = 2 * (which ? p.v_st : p.k_st);
     const uint32_t to = lds0 + (which ? V0 : 0) + buf * TB + wv * 1024;
-    if (key0 + BN <= s.kn) {
+    if (key0 >= key_first && key0 + BN <= s.kn) {
 #pragma unroll
       for (int i = 0; i < LD; ++i) fetch_one(which, buf, key0, i);
     } else {
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
         const int c0 = D == 512 ? here() : tid % C;
         const int c = c0 ^ (which ? v_swz<D>(r0 + RS * i) : k_swz<D>(r0 + RS * i));
         load_lds16(to + i * TH * 16, base + key0 * st,
-                   (uint32_t)(min(r0 + RS * i, s.kn - 1 - key0) * (int)st + 16 * c));
+                   (uint32_t)(min(max(r0 + RS * i, key_first - key0), s.kn - 1 - key0) * (int)st + 16 * c));
       }
     }
   };

@@ -1,0 +1,67 @@
+"""Edges of the attention operators' contract (include/moe_attn.h): what lies in
+places that no row keeps, caches of one tensor, streams, and sizes at the ends of the declared
+ranges.  Bounds are those of test_gpu_attention."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import dev, dev_bf16
+from oracle import attention
+from test_gpu_attention import _Paged, _check, _cu, _f, _vals
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("block_scaled_fp4_sqrtsoftplus_amd")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,dim,shared", [
+    (4, 2, 64, False), (6, 2, 128, False), (4, 2, 256, False), (3, 1, 512, False), (8, 1, 512, True)])
+def test_prefill_does_not_read_keys_before_every_window(hq, hkv, dim, shared, causal):
+    # a window over a context: the keys before the first row's window (91, 102 and 14 of them, inside the tile that
+    # the first kept key lies in) hold NaN and infinities
+    rng = np.random.default_rng(dim + hq + causal)
+    q_lens, k_lens, window = [40, 129, 7], [200, 300, 90], 70
+    q, k = _vals(rng, sum(q_lens), hq, dim), _vals(rng, sum(k_lens), hkv, dim)
+    v = k if shared else _vals(rng, sum(k_lens), hkv, dim)
+    cq, ck = _cu(q_lens), _cu(k_lens)
+    for b, (n, m) in enumerate(zip(q_lens, k_lens)):
+        before = m - n + 1 - window
+        assert 0 < before < m and before % 32
+        for x in (k, v):
+            x[ck[b]:ck[b] + before] = 0x7FC0                 # NaN
+            x[ck[b]:ck[b] + before:3] = 0x7F80               # infinity
+            x[ck[b] + 1:ck[b] + before:3] = 0xFF80
+    kd = dev_bf16(k)
+    out, lse = moe.attn_prefill(dev_bf16(q), kd, kd if shared else dev_bf16(v), dev(cq), dev(ck), causal, window,
+                                want_lse=True)
+    torch.cuda.synchronize()
+    parts = []
+    for b in range(3):
+        rows = [_f(x[ck[b]:ck[b + 1]]).swapaxes(0, 1) for x in (k, v)]
+        with np.errstate(invalid="ignore"):
+            parts.append(attention.attend(_f(q[cq[b]:cq[b + 1]]), *rows, k_lens[b] - q_lens[b], dim ** -0.5, causal,
+                                          window))
+    _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)
+
+
+
+@pytest.mark.parametrize("hq,dim,page,q_len,fp8", [
+    (4, 128, 16, 2, False), (4, 64, 64, 1, True), (24, 128, 16, 2, False), (24, 256, 32, 1, True), (64, 512, 16, 3, False)])
+def test_decode_does_not_read_keys_before_every_window(hq, dim, page, q_len, fp8):
+    rng = np.random.default_rng(dim + hq)
+    lens, window = [500, 77, 2000], 45
+    p = _Paged(rng, lens, 1, dim, page, fp8)
+    for b, n in enumerate(lens):
+        at = np.arange(n - q_len + 1 - window)
+        pages, rows = (dev(x.astype(np.int64)) for x in (p.table[b, at // page], at % page))
+        for x, scale in ((p.cache.k, p.cache.k_scale), (p.cache.v, p.cache.v_scale)):
+            x[pages, :, rows] = 0x7F if fp8 else float("nan")
+            x[pages[::3], :, rows[::3]] = 0x7F if fp8 else float("inf")
+            if fp8:
+                scale[pages, :, rows] = 255
+    q = _vals(rng, len(lens) * q_len, hq, dim)
+    out, lse = moe.attn_decode(dev_bf16(q), p.cache, dev(p.table), dev(p.lens), q_len, window, want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, p.reference(q, q_len, dim ** -0.5, window), dim)
