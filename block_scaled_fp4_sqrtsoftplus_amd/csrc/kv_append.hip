@@ -37,6 +37,7 @@ struct AppendArgs {
   char* cv;
   uint8_t* cks;
   uint8_t* cvs;
+  uint8_t* cks2;             // the values' scales where one tensor of codes has two arrays of them, or null
   int64_t c_sp, c_sh, c_st;  // elements
   int64_t slots_end;         // pages * page_size
   int page_shift;
@@ -162,8 +163,10 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs p) {
         *reinterpret_cast<u32x2*>(dst + at) = code;
         if (c % GROUP == 0) {
           uint8_t* sc = is_k ? p.cks : p.cvs;
-          sc[((page * p.hk + h) * (int64_t(1) << p.page_shift) + in_page) * NG + c / GROUP] =
-              (uint8_t)(e + 127);
+          const int64_t i =
+              ((page * p.hk + h) * (int64_t(1) << p.page_shift) + in_page) * NG + c / GROUP;
+          sc[i] = (uint8_t)(e + 127);
+          if (p.cks2) p.cks2[i] = (uint8_t)(e + 127);
         }
       }
     }
@@ -185,6 +188,7 @@ hipError_t launch_kv_append(const moe_kv_cache& c, const moe_rope* rope, int64_t
   if (k_out) { a.k_out = k_out->p; a.ko_st = k_out->stride_token; a.ko_sh = k_out->stride_head; }
   a.ck = static_cast<char*>(c.k); a.cv = static_cast<char*>(c.v);
   a.cks = c.k_scale; a.cvs = c.v_scale;
+  a.cks2 = !v && c.v_scale != c.k_scale ? c.v_scale : nullptr;
   a.c_sp = c.stride_page; a.c_sh = c.stride_head; a.c_st = c.stride_token;
   a.slots_end = c.pages * c.page_size;
   a.page_shift = __builtin_ctz((unsigned)c.page_size);

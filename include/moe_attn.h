@@ -57,7 +57,8 @@ typedef struct moe_rows {
 /* A paged cache: page, head, row in the page, element.  Position j of a
  * sequence with block table row `table` is row j % page_size of page
  * table[j / page_size].  v == k is a cache of one tensor that serves as keys and
- * values (a latent cache). */
+ * values (a latent cache).  An FP8 one may have two arrays of scales, whose
+ * values are then the keys' codes under v_scale; the append gives both a new row's scales. */
 typedef struct moe_kv_cache {
   void* k;
   void* v;

@@ -65,3 +65,27 @@ def test_decode_does_not_read_keys_before_every_window(hq, dim, page, q_len, fp8
     out, lse = moe.attn_decode(dev_bf16(q), p.cache, dev(p.table), dev(p.lens), q_len, window, want_lse=True)
     torch.cuda.synchronize()
     _check(out, lse, p.reference(q, q_len, dim ** -0.5, window), dim)
+
+
+# ----------------------------------------------------------------------------
+# Caches of one tensor
+# ----------------------------------------------------------------------------
+
+
+def test_append_writes_both_scales_of_one_tensor():
+    # one tensor of codes under two arrays of scales: a new row's scales go into both, so that its values are its keys
+    rng = np.random.default_rng(71)
+    n, dim, page = 40, 256, 16
+    cache = moe.KVCache.empty(4, page, 1, dim, moe.KV_FP8, shared=True)
+    values = torch.full_like(cache.k_scale, 9)
+    cache.c.v_scale = values.data_ptr()
+    slots = rng.permutation(4 * page)[:n].astype(np.int64)
+    slots[5] = -1
+    moe.kv_append(cache, dev_bf16(_vals(rng, n, 1, dim, scale=30.0)), None, dev(slots))
+    torch.cuda.synchronize()
+    stored = dev(slots[slots >= 0])
+    keys, values = (t.permute(0, 2, 1, 3).reshape(4 * page, -1) for t in (cache.k_scale, values))
+    assert (keys[stored] > 100).all() and torch.equal(values[stored], keys[stored])
+    others = torch.ones(4 * page, dtype=torch.bool, device="cuda")
+    others[stored] = False
+    assert (values[others] == 9).all() and (keys[others] == 0).all()
