@@ -71,29 +71,35 @@ class KVCache:
 
     k, v [pages, heads, page_size, head_dim]: bf16, or FP8 (uint8 E4M3 codes or
     float8_e4m3fn) with k_scale, v_scale [pages, heads, page_size,
-    max(1, head_dim // 128)] uint8 E8M0 bytes.  v None or k itself: one tensor
-    serves as keys and values.  Any strides over the first three indices that
+    max(1, head_dim // 128)] uint8 E8M0 bytes.  v None or k itself (or its very
+    elements): one tensor serves as keys and values, under the keys' scales unless v_scale
+    is given too.  Any strides over the first three indices that
     k and v share, such as those of [pages, page_size, heads, head_dim]
     transposed."""
 
     def __init__(self, k, v=None, k_scale=None, v_scale=None):
-        self.shared = v is None or v is k or v.data_ptr() == k.data_ptr()
-        if self.shared:
-            v, v_scale = k, k_scale
-        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        if v is None:
+            v = k
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        if k.dim() != 4 or v.shape != k.shape or v.device != k.device or \
+                v.dtype != k.dtype and not (k.dtype in codes and v.dtype in codes):
             raise ValueError("k and v must be alike, [pages, heads, page_size, head_dim]")
         if not k.is_cuda:
             raise ValueError("tensors passed to the HIP library must be on the GPU")
         if k.dtype is torch.bfloat16:
             self.format = KV_BF16
-            if k_scale is not None:
+            if k_scale is not None or v_scale is not None:
                 raise ValueError("a bf16 cache has no scales")
-        elif k.dtype in (torch.uint8, torch.float8_e4m3fn):
+        elif k.dtype in codes:
             self.format = KV_FP8
         else:
             raise ValueError("a cache is bfloat16, or uint8 / float8_e4m3fn with scales")
-        if k.stride() != v.stride() or k.stride(3) != 1:
+        if any(n > 1 and a != b for n, a, b in zip(k.shape, k.stride(), v.stride())) or k.stride(3) != 1:
             raise ValueError("k and v must share their strides and be contiguous in the last index")
+        # one tensor, if not one object: the same elements (an empty tensor has no address)
+        self.shared = v is k or (k.numel() > 0 and v.data_ptr() == k.data_ptr())
+        if self.shared:
+            v, v_scale = k, k_scale if v_scale is None else v_scale
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale

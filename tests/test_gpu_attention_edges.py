@@ -89,3 +89,48 @@ def test_append_writes_both_scales_of_one_tensor():
     others = torch.ones(4 * page, dtype=torch.bool, device="cuda")
     others[stored] = False
     assert (values[others] == 9).all() and (keys[others] == 0).all()
+
+
+def test_cache_keeps_what_it_is_given():
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    k = torch.zeros((4, 2, 16, 128), **u8)
+    ks, vs = torch.zeros((4, 2, 16, 1), **u8), torch.ones((4, 2, 16, 1), **u8)
+    for v in (None, k, k.view(4, 2, 16, 128), k.view(torch.float8_e4m3fn)):
+        c = moe.KVCache(k, v, ks, vs)
+        assert c.shared and c.v is c.k
+        assert (c.c.k_scale, c.c.v_scale) == (ks.data_ptr(), vs.data_ptr()) and c.v_scale is vs
+        c = moe.KVCache(k, v, ks)
+        assert c.shared and (c.c.k_scale, c.c.v_scale) == (ks.data_ptr(), ks.data_ptr())
+    # values that lie at the keys' address in another layout are not the keys
+    for v in (k[:2], k[..., :64], k.view(4, 16, 2, 128).transpose(1, 2), k.view(torch.bfloat16)):
+        assert v.data_ptr() == k.data_ptr()
+        with pytest.raises(ValueError, match="k and v"):
+            moe.KVCache(k, v, ks, vs)
+    with pytest.raises(ValueError, match="scale"):
+        moe.KVCache(k, None, ks, vs[:2])
+    with pytest.raises(ValueError, match="scale"):
+        moe.KVCache(k, torch.zeros_like(k), ks)
+    b = torch.zeros((4, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    for scales in (dict(k_scale=ks), dict(v_scale=vs)):
+        with pytest.raises(ValueError, match="scales"):
+            moe.KVCache(b, **scales)
+    # strides over indices of one value are free, and empty tensors share no address
+    one = torch.zeros((1, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    moe.KVCache(one, torch.zeros((2, 2, 16, 128), dtype=torch.bfloat16, device="cuda")[1:])
+    assert not moe.KVCache.empty(0, 16, 2, 64).shared
+
+
+@pytest.mark.parametrize("hq,dim", [(8, 128), (64, 512)])
+def test_values_under_their_own_scales(hq, dim):
+    # the values are the keys' codes, four times as large
+    rng = np.random.default_rng(hq)
+    lens = [400, 33, 0]
+    p = _Paged(rng, lens, 1, dim, 16, fp8=True, shared=True)
+    scales = p.cache.k_scale.clone()
+    scales[scales != 255] += 2
+    cache = moe.KVCache(p.cache.k, None, p.cache.k_scale, scales)
+    p.v = p.v * 4
+    q = _vals(rng, 3, hq, dim)
+    out, lse = moe.attn_decode(dev_bf16(q), cache, dev(p.table), dev(p.lens), want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, p.reference(q, 1, dim ** -0.5), dim)
