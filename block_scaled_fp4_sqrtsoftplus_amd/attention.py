@@ -173,7 +173,8 @@ class DecodeAttention:
     """Holds the sizes, the cache and the workspace of moe_attn_decode and runs
     it on the current stream: attention of every sequence's newest q_len tokens
     over the cache, which holds them already.  Calls that may overlap, on other
-    streams, need an object each: they would share the workspace."""
+    streams, need an object each: they would share the workspace.  The object may go
+    while calls are still running; a graph that recorded one needs it as long as it is replayed."""
 
     def __init__(self, cache: KVCache, batch, heads_q, q_len=1, window=0, scale=None):
         self.cache, self.batch, self.heads_q, self.q_len = cache, batch, heads_q, q_len
@@ -184,13 +185,18 @@ class DecodeAttention:
         self.ws_bytes = lib.moe_attn_workspace_size(_byref(self.c))
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=cache.device)
         self._ws = self.ws.data_ptr()
+        self._streams = {_raw_stream(self._index)}   # those the allocator knows the workspace to be used on
 
     def __call__(self, q, block_table, seq_lens, out=None, want_lse=False):
         """q [batch * q_len, heads_q, head_dim] bf16, block_table [batch, width]
         int32, seq_lens [batch] int32 (new tokens included): out like q, and
         with want_lse also lse [batch * q_len, heads_q] fp32."""
         index = self._index
-        return _native.attn_decode(self._at, self.cache._at, index, _raw_stream(index), self._ws, self.ws_bytes, q,
+        stream = _raw_stream(index)
+        if stream not in self._streams:
+            self.ws.record_stream(torch.cuda.current_stream(index))
+            self._streams.add(stream)
+        return _native.attn_decode(self._at, self.cache._at, index, stream, self._ws, self.ws_bytes, q,
                                    block_table, seq_lens, out, want_lse)
 
 

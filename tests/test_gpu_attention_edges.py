@@ -134,3 +134,30 @@ def test_values_under_their_own_scales(hq, dim):
     out, lse = moe.attn_decode(dev_bf16(q), cache, dev(p.table), dev(p.lens), want_lse=True)
     torch.cuda.synchronize()
     _check(out, lse, p.reference(q, 1, dim ** -0.5), dim)
+
+
+# ----------------------------------------------------------------------------
+# Streams
+# ----------------------------------------------------------------------------
+
+
+def test_workspace_is_kept_for_the_stream_it_is_used_on():
+    # the object goes while its call still waits on a side stream: its workspace must not be given away
+    rng = np.random.default_rng(73)
+    p = _Paged(rng, [900, 5000], 2, 128, 16)
+    q, table, lens = dev_bf16(_vals(rng, 2, 4, 128)), dev(p.table), dev(p.lens)
+    a = moe.DecodeAttention(p.cache, 2, 4)
+    want = a(q, table, lens)
+    size, at = a.ws.numel(), a.ws.data_ptr()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)       # some ms in which the host goes on
+        got = a(q, table, lens)
+    del a
+    other = torch.empty(size, dtype=torch.uint8, device="cuda")
+    given_away = other.data_ptr() == at
+    if not given_away:
+        other.fill_(0xFF)
+    torch.cuda.synchronize()
+    assert not given_away and torch.equal(got, want)
