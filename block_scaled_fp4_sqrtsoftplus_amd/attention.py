@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import MoeError, _i32, _i64, _ptr, _sz, _vp, lib
+from . import STATUS_NAMES, MoeError, _i32, _i64, _ptr, _sz, _vp, lib
 from . import _attn_binding as _native
 
 KV_BF16, KV_FP8 = 0, 1
@@ -59,6 +59,16 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _native.set_error(MoeError)
 
 
+def _fit(*sizes):
+    """Whether the C structs' 32-bit fields hold these: ctypes would drop their upper bits."""
+    return all(-(1 << 31) <= n < 1 << 31 for n in sizes)
+
+
+def _check_fit(*sizes):
+    if not _fit(*sizes):
+        raise MoeError(STATUS_NAMES.index("MOE_ERR_BAD_SHAPE"))
+
+
 def _bytes_at(t, shape, device, name):
     """The address of a contiguous uint8 tensor on `device`."""
     if t.dtype is not torch.uint8 or t.shape != shape or t.device != device:
@@ -101,6 +111,7 @@ class KVCache:
         if self.shared:
             v, v_scale = k, k_scale if v_scale is None else v_scale
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        _check_fit(self.heads, self.page_size, self.head_dim)
         self.device = k.device
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         ks = vs = None
@@ -137,6 +148,7 @@ class Rope:
     def __init__(self, cos_sin, rot_offset=0, interleaved=False):
         if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [positions, rot_dim]")
+        _check_fit(cos_sin.shape[1], rot_offset)
         self.cos_sin, self.device = cos_sin, cos_sin.device
         self.c = MoeRopeC(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], rot_offset, int(interleaved), 0)
         self._at, self._index = ctypes.addressof(self.c), self.device.index
@@ -165,6 +177,8 @@ def kv_append(cache: KVCache, k, v, slots, positions=None, rope: Rope = None, q=
 
 def attn_workspace_size(batch, heads_q, heads_kv, head_dim, q_len=1):
     """Bytes of workspace moe_attn_decode needs (0 for an invalid configuration)."""
+    if not _fit(batch, q_len, heads_q, heads_kv, head_dim):
+        return 0
     c = MoeAttnConfigC(batch * q_len, 0, batch, q_len, heads_q, heads_kv, head_dim, 1, 0, 1.0)
     return lib.moe_attn_workspace_size(_byref(c))
 
@@ -177,6 +191,7 @@ class DecodeAttention:
     while calls are still running; a graph that recorded one needs it as long as it is replayed."""
 
     def __init__(self, cache: KVCache, batch, heads_q, q_len=1, window=0, scale=None):
+        _check_fit(batch, q_len, heads_q, window)
         self.cache, self.batch, self.heads_q, self.q_len = cache, batch, heads_q, q_len
         self.tokens = batch * q_len
         scale = cache.head_dim ** -0.5 if scale is None else scale

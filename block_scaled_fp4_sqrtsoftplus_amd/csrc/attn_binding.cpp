@@ -164,6 +164,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& qt = tensor(a[8], "q");
     q = rows(qt, tokens, -1, dim, index, "q");
     hq = qt.size(1);
+    if (hq > INT32_MAX) return failed(MOE_ERR_BAD_SHAPE);
     out = a[9] == Py_None ? fresh({tokens, hq, dim}, at::kBFloat16, index) : tensor(a[9], "q_out");
     qo = rows(out, tokens, hq, dim, index, "q_out");
   } else if (a[9] != Py_None) {

@@ -161,3 +161,28 @@ def test_workspace_is_kept_for_the_stream_it_is_used_on():
         other.fill_(0xFF)
     torch.cuda.synchronize()
     assert not given_away and torch.equal(got, want)
+
+
+# ----------------------------------------------------------------------------
+# Refusals
+# ----------------------------------------------------------------------------
+
+
+def test_sizes_past_32_bits_are_refused():
+    # they must not lose their upper bits on the way into the C structs
+    cache = moe.KVCache.empty(2, 16, 2, 64)
+    far = 1 << 32
+    for kw in (dict(window=far + 5), dict(window=-far), dict(q_len=far + 1), dict(batch=far + 1),
+               dict(heads_q=far + 2)):
+        with pytest.raises(moe.MoeError, match="SHAPE"):
+            moe.DecodeAttention(cache, **{**dict(batch=1, heads_q=2), **kw})
+    table = torch.zeros((10, 64), device="cuda")
+    with pytest.raises(moe.MoeError, match="SHAPE"):
+        moe.Rope(table, rot_offset=far)
+    wide = torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16, device="cuda").expand(1, far + 1, 16, 64)
+    with pytest.raises(moe.MoeError, match="SHAPE"):
+        moe.KVCache(wide)
+    none = torch.zeros((0, 1, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(moe.MoeError, match="SHAPE"):
+        moe.kv_append(cache, none.expand(0, 2, 64), none.expand(0, 2, 64),
+                      torch.zeros(0, dtype=torch.int64, device="cuda"), q=none.expand(0, far + 1, 64))
