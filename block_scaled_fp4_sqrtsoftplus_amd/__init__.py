@@ -22,9 +22,9 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_fp4.so")
 
-if not (os.path.exists(LIB_PATH) and os.path.exists(os.path.join(_PKG, "_attn_binding.so"))):
+if not os.path.exists(LIB_PATH):
     raise ImportError(
-        f"{LIB_PATH} (or _attn_binding.so beside it) is missing: build it with `python block_scaled_fp4_sqrtsoftplus_amd/build.py` "
+        f"{LIB_PATH} is missing: build it with `python block_scaled_fp4_sqrtsoftplus_amd/build.py` "
         "(hipcc, gfx950); this package has no non-HIP fallback")
 
 lib = ctypes.CDLL(LIB_PATH)
@@ -327,5 +327,20 @@ def layer(cfg: Config, x, weights, w_gate=None, bias=None, token_ids=None, share
     return (y, routing) if want_routing else y
 
 
-from .attention import (  # noqa: E402,F401
-    KV_BF16, KV_FP8, DecodeAttention, KVCache, Rope, attn_decode, attn_prefill, attn_workspace_size, kv_append)
+# The attention operators' binding has a native half that is tied to the torch
+# it was built against.  Without it the layer works as before, and each of these names raises the
+# reason when it is used.
+_ATTENTION = ("KV_BF16", "KV_FP8", "DecodeAttention", "KVCache", "Rope", "attn_decode", "attn_prefill",
+              "attn_workspace_size", "kv_append")
+try:
+    from .attention import (  # noqa: E402,F401
+        KV_BF16, KV_FP8, DecodeAttention, KVCache, Rope, attn_decode, attn_prefill, attn_workspace_size, kv_append)
+except ImportError as _why:
+    _no_attention = str(_why)
+
+    def __getattr__(name):
+        if name in _ATTENTION:
+            raise ImportError(
+                f"{__name__}.{name} needs _attn_binding.so beside {LIB_PATH}, which does not load ({_no_attention}): "
+                "build it with `python block_scaled_fp4_sqrtsoftplus_amd/build.py`")
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
