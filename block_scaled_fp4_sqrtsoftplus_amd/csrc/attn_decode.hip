@@ -64,6 +64,7 @@ struct DecodeArgs {
   int window;
   float scale2;            // scale * log2(e)
   int pieces;              // the work's, for one head and row group; 0: one per sequence
+  uint32_t first;          // the launch's first workgroup
   int tile_shift;          // keys per tile, the unit of the cut: 2^tile_shift
   float* part_o;           // [pieces + batch][hkv][rows][D]
   float* part_m;           // [pieces + batch][hkv][rows] maximum (base 2)
@@ -334,8 +335,9 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
   const int col = lane & 15, g = lane >> 4;
   const int kp = wave;
 
-  const int piece = blockIdx.x / p.hkv;
-  const int h = blockIdx.x - piece * p.hkv;
+  const uint32_t wg = p.first + blockIdx.x;
+  const int piece = wg / p.hkv;
+  const int h = wg - piece * p.hkv;
   constexpr int rg = 0;
   Piece pc;
   if (!find_piece<true>(p, piece, pc)) return;
@@ -608,8 +610,9 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
   const int rt = wave % RT, kp = wave / RT;
 
   const int per_piece = p.hkv * p.rgroups;
-  const int piece = blockIdx.x / per_piece;
-  const int rest = blockIdx.x - piece * per_piece;
+  const uint32_t wg = p.first + blockIdx.x;
+  const int piece = wg / per_piece;
+  const int rest = wg - piece * per_piece;
   const int rg = rest / p.hkv, h = rest - rg * p.hkv;
   Piece pc;
   if (!find_piece<false>(p, piece, pc)) return;
@@ -825,8 +828,9 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
   __shared__ f32x4 so[NGR][GL];
   __shared__ float sm[NGR], sl[NGR];
   const uint32_t per_b = (uint32_t)(p.hkv * p.rows);
-  const uint32_t b = blockIdx.x / per_b;
-  const int rest = (int)(blockIdx.x - b * per_b);
+  const uint32_t wg = p.first + blockIdx.x;
+  const uint32_t b = wg / per_b;
+  const int rest = (int)(wg - b * per_b);
   const int h = rest / p.rows, row = rest - h * p.rows;
   const int2 mt = p.meta[b];
   if (mt.y <= 1) return;
@@ -954,7 +958,7 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   a.part_l = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.meta = reinterpret_cast<int2*>(w);
   const int64_t cut = row_tiles(d.rows, c.head_dim) == 1 ? d.pieces : d.slots;
-  const dim3 grid((unsigned)((whole ? c.batch : cut) * c.heads_kv * d.rgroups));
+  const int64_t workgroups = (whole ? c.batch : cut) * c.heads_kv * d.rgroups;
   const int rt = row_tiles(d.rows, c.head_dim);
   const bool f8 = kv.format == MOE_KV_FP8;
 #define MOE_ROWS(D, F, R, KP, O)                                                              \
@@ -976,33 +980,35 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
   case D:                                                                                     \
     if (f8) MOE_FEW(D, true); else MOE_FEW(D, false);                                         \
     break;
-  switch (c.head_dim) {
-    MOE_DECODE(64) MOE_DECODE(128)
-    case 256:
-      if (rt == 1) {
-        if (f8) MOE_DIRECT(256, true); else MOE_DIRECT(256, false);
+  hipError_t e = launch_workgroups(workgroups, [&](uint32_t first, dim3 grid) {
+    a.first = first;
+    switch (c.head_dim) {
+      MOE_DECODE(64) MOE_DECODE(128)
+      case 256:
+        if (rt == 1) {
+          if (f8) MOE_DIRECT(256, true); else MOE_DIRECT(256, false);
+          break;
+        }
+        if (f8) MOE_ROWS_ANY(256, true, 4); else MOE_ROWS_ANY(256, false, 4);
         break;
-      }
-      if (f8) MOE_ROWS_ANY(256, true, 4); else MOE_ROWS_ANY(256, false, 4);
-      break;
-    case 512:
-      if (f8) MOE_ROWS_ANY(512, true, 4); else MOE_ROWS_ANY(512, false, 4);
-      break;
-    default: return hipErrorInvalidValue;
-  }
+      case 512:
+        if (f8) MOE_ROWS_ANY(512, true, 4); else MOE_ROWS_ANY(512, false, 4);
+        break;
+    }
+  });
 #undef MOE_DECODE
 #undef MOE_FEW
 #undef MOE_DIRECT
 #undef MOE_ROWS_ANY
 #undef MOE_ROWS
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole) return e;
-  const dim3 jgrid((unsigned)((int64_t)c.batch * c.heads_kv * d.rows));
 #define MOE_JOIN(D) \
-  case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), jgrid, dim3(256), 0, st, a); break;
-  switch (c.head_dim) { MOE_JOIN(64) MOE_JOIN(128) MOE_JOIN(256) MOE_JOIN(512) }
+  case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), grid, dim3(256), 0, st, a); break;
+  return launch_workgroups((int64_t)c.batch * c.heads_kv * d.rows, [&](uint32_t first, dim3 grid) {
+    a.first = first;
+    switch (c.head_dim) { MOE_JOIN(64) MOE_JOIN(128) MOE_JOIN(256) MOE_JOIN(512) }
+  });
 #undef MOE_JOIN
-  return hipGetLastError();
 }
 
 }  // namespace moe

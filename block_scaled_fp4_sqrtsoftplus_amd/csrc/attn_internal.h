@@ -104,6 +104,21 @@ __device__ __forceinline__ void arrived(const T& x) {
 // exponent hold as well, and the output is seldom rescaled.
 constexpr float kLag = 8.f;
 
+// A launch takes less than 2^32 work-items: more workgroups than that go out in
+// several, each of which is told the number of its first one.  2^22 of up to
+// 512 work-items each, and a multiple of the 8 XCDs that workgroups go to in turn.
+template <class Launch>
+hipError_t launch_workgroups(int64_t count, Launch launch) {
+  constexpr int64_t kMost = int64_t(1) << 22;
+  for (int64_t first = 0; first < count; first += kMost) {
+    const int64_t n = count - first < kMost ? count - first : kMost;
+    launch((uint32_t)first, dim3((unsigned)n));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // Device check and cached properties (api.cpp).
 moe_status device_ok();
 

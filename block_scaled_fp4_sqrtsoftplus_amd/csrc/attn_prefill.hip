@@ -45,6 +45,7 @@ struct PrefillArgs {
   const int32_t* cu_k;
   int64_t tokens, tokens_kv;
   int batch, hq, hkv, group, causal, window;
+  uint32_t first;         // the launch's first workgroup
   uint32_t q_flip;        // sign bits to flip in q: scale2 is |scale| log2(e)
   float scale2;
 };
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   // workgroups go to the 8 XCDs in turn: a key-value head stays on one XCD
   int h, tile;
   {
-    const int w = blockIdx.x;
+    const int w = p.first + blockIdx.x;
     if (p.hkv % 8 == 0) {
       const int per = p.hkv / 8, i = w >> 3;
       h = (w & 7) * per + i % per;
@@ -639,9 +640,11 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
   {                                                                                           \
     /* at most one partly filled tile per sequence */                                         \
     const int64_t tiles = c.tokens * a.group / (32 * RG) + std::min<int64_t>(c.batch, c.tokens); \
-    hipLaunchKernelGGL((attn_prefill_kernel<D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES, ONE>),            \
-                       dim3((unsigned)(tiles * c.heads_kv)), dim3(64 * RG * SPLIT), 0, st, a); \
-    break;                                                                                    \
+    return launch_workgroups(tiles * c.heads_kv, [&](uint32_t first, dim3 grid) {             \
+      a.first = first;                                                                        \
+      hipLaunchKernelGGL((attn_prefill_kernel<D, BN, RG, SPLIT, BUFS, PIPE, AHEAD, WAVES, ONE>), grid, \
+                         dim3(64 * RG * SPLIT), 0, st, a);                                    \
+    });                                                                                       \
   }
   // Weights beside the next step's products, or not (PIPE), in us: 64-element heads,
   // 8192 tokens 343 and 315 (without it four workgroups share a CU); 128, 8192 tokens
@@ -656,11 +659,9 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
         MOE_PREFILL(512, 32, 4, 2, 3, false, 2, 2, true)
       else
         MOE_PREFILL(512, 32, 4, 2, 2, false, 2, 2, false)
-      break;
     default: return hipErrorInvalidValue;
   }
 #undef MOE_PREFILL
-  return hipGetLastError();
 }
 
 }  // namespace moe

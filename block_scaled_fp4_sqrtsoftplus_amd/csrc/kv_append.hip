@@ -49,6 +49,7 @@ struct AppendArgs {
   int rot_dim, rot_offset, interleaved;
   int hq, hk, hv;            // heads of q, k and v to go through
   int parts;                 // waves that share one token's heads
+  uint32_t first;            // the launch's first workgroup
 };
 
 // lane's 8 elements rotated (see the formulas above); partner values by
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs p) {
   constexpr int GROUP = D < 128 ? D / 8 : 16;   // lanes per FP8 scale
   constexpr int NG = D < 128 ? 1 : D / 128;
   const int lane = threadIdx.x & 63;
-  const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t wave = ((int64_t)p.first + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int64_t t = wave / p.parts;
   const int part = (int)(wave - t * p.parts);
   if (t >= p.tokens) return;
@@ -211,7 +212,6 @@ hipError_t launch_kv_append(const moe_kv_cache& c, const moe_rope* rope, int64_t
   // caches and 94 through them, 50 MB the same, 12 MB 9.8 and 7.3.
   const bool stream = tokens * (a.hq + a.hk + a.hv) * c.head_dim * 2 > (int64_t(64) << 20);
   const int64_t waves = tokens * a.parts;
-  const dim3 grid((unsigned)((waves + 3) / 4));
 #define MOE_APPEND_S(D, F)                                                                   \
   do {                                                                                       \
     if (stream)                                                                              \
@@ -223,13 +223,14 @@ hipError_t launch_kv_append(const moe_kv_cache& c, const moe_rope* rope, int64_t
   case D:                                                                                    \
     if (c.format == MOE_KV_FP8) MOE_APPEND_S(D, true); else MOE_APPEND_S(D, false);          \
     break;
-  switch (c.head_dim) {
-    MOE_APPEND(64) MOE_APPEND(128) MOE_APPEND(256) MOE_APPEND(512)
-    default: return hipErrorInvalidValue;
-  }
+  return launch_workgroups((waves + 3) / 4, [&](uint32_t first, dim3 grid) {
+    a.first = first;
+    switch (c.head_dim) {
+      MOE_APPEND(64) MOE_APPEND(128) MOE_APPEND(256) MOE_APPEND(512)
+    }
+  });
 #undef MOE_APPEND
 #undef MOE_APPEND_S
-  return hipGetLastError();
 }
 
 }  // namespace moe

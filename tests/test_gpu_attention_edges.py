@@ -9,6 +9,7 @@ import torch
 from gpu_util import dev, dev_bf16
 from oracle import attention
 from test_gpu_attention import _Paged, _check, _cu, _f, _vals
+from test_gpu_attention_paths import splits_of
 
 pytestmark = pytest.mark.gpu
 
@@ -186,3 +187,77 @@ def test_sizes_past_32_bits_are_refused():
     with pytest.raises(moe.MoeError, match="SHAPE"):
         moe.kv_append(cache, none.expand(0, 2, 64), none.expand(0, 2, 64),
                       torch.zeros(0, dtype=torch.int64, device="cuda"), q=none.expand(0, far + 1, 64))
+
+
+# ----------------------------------------------------------------------------
+# Grids past 2^32 work-items
+# ----------------------------------------------------------------------------
+
+
+def _spread(x):
+    """Bits of a tensor's rows summed per row, to compare many rows of the same inputs cheaply."""
+    return x.view(torch.int16).flatten(1).long().sum(1)
+
+
+def test_append_of_more_tokens_than_a_launch_takes():
+    # 2^26 tokens and some, one wave each; all but the first and last three are padding
+    n, dim = (1 << 26) + 5, 64
+    cache = moe.KVCache.empty(1, 16, 1, dim, shared=True)
+    k = torch.arange(dim, device="cuda").bfloat16().view(1, 1, dim).expand(n, 1, dim)
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    slots[:3], slots[-3:] = torch.arange(3), torch.arange(5, 8)
+    moe.kv_append(cache, k, None, slots)
+    torch.cuda.synchronize()
+    rows = cache.k[0, 0]
+    for i in range(16):
+        assert torch.equal(rows[i], k[0, 0] if i in (0, 1, 2, 5, 6, 7) else torch.zeros_like(rows[i])), i
+
+
+@pytest.mark.parametrize("batch,q_len,hq,hkv,width", [
+    (65536, 16, 16, 16, 160),      # the join of cut sequences: a workgroup per row, 2^24 of them
+    (16384, 1, 1024, 1024, 2),     # a workgroup per sequence and head, 2^24 of them
+])
+def test_decode_of_more_rows_than_a_launch_takes(batch, q_len, hq, hkv, width):
+    # every sequence has the same keys and the same queries, but for its length: 3, 40 or 19
+    rng = np.random.default_rng(75)
+    dim, page = 64, 16
+    p = _Paged(rng, [48], hkv, dim, page)
+    q = dev_bf16(_vals(rng, q_len, hq, dim))
+    lens = torch.tensor([3, 40, 19], dtype=torch.int32, device="cuda").repeat(batch // 3 + 1)[:batch].contiguous()
+    lens[0], lens[-1] = 19, 40
+    if width > 3:
+        lens[2030:2060] = width * page                      # most of it on no page; some are cut
+    table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+    wide = min(width, p.table.shape[1])
+    table[:, :wide] = dev(p.table)[:, :wide]
+    lens.clamp_(max=width * page)
+    many = q.repeat(batch, 1, 1)
+    a = moe.DecodeAttention(p.cache, batch, hq, q_len)
+    out = a(many, table, lens)
+    torch.cuda.synchronize()
+    assert (splits_of(a)[1] > 1).any() == (width > 3)
+    sums = _spread(out).view(batch, q_len)
+    del many, a
+    for n in lens.unique().tolist():
+        which = (lens == n).nonzero().flatten()
+        b = int(which[0])
+        one = moe.attn_decode(q, p.cache, table[b:b + 1].contiguous(), lens[b:b + 1].contiguous(), q_len)
+        if n > 64:      # the order of its sums depends on where it is cut: both round weights and outputs to bf16
+            got = out.view(batch, q_len, hq, dim)[which].float()
+            assert (got - one.float()).abs().max() <= 4 * 2.0 ** -8 * 1.01 * np.nanmax(np.abs(p.v))
+        else:
+            assert torch.equal(sums[which], _spread(one).expand(len(which), q_len)), n
+    del out
+    torch.cuda.empty_cache()
+
+
+def test_prefill_of_more_tiles_than_a_launch_takes():
+    # 16384 prompts of one token, 1024 heads: each output is its value
+    n, heads, dim = 16384, 1024, 64
+    x = torch.randn((n, heads, dim), device="cuda", dtype=torch.bfloat16)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out = moe.attn_prefill(x, x, x, cu)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
+    del out, x
+    torch.cuda.empty_cache()
