@@ -297,7 +297,7 @@ __device__ __forceinline__ void finish(const DecodeArgs& p, const Part& pc, int 
     p.meta[pc.b] = make_int2(pc.slot, pc.splits);
   if (!row_live) return;
   if (pc.splits == 1) {
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
     uint16_t* dst = p.out + qrow * p.o_st + head * p.o_sh;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -305,7 +305,7 @@ __device__ __forceinline__ void finish(const DecodeArgs& p, const Part& pc, int 
       *reinterpret_cast<u32x2*>(dst + col(i)) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     }
     if (p.lse && g == 0)
-      p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      p.lse[qrow * p.hq + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   } else {
     const int64_t idx = ((int64_t)pc.slot * p.hkv + h) * p.rows + row;
     float* dst = p.part_o + idx * D;
@@ -869,7 +869,7 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
     l += sl[i] * a;
   }
   m = top;
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
   o *= inv;
   const int tok = row / p.group;
   const int head = h * p.group + row - tok * p.group;
@@ -877,7 +877,7 @@ __global__ __launch_bounds__(256) void attn_decode_join_kernel(DecodeArgs p) {
   *reinterpret_cast<u32x2*>(p.out + qrow * p.o_st + head * p.o_sh + gl * 4) =
       u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
   if (p.lse && gl == 0)
-    p.lse[qrow * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    p.lse[qrow * p.hq + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 // Row tiles of a workgroup; 1: the kernel without LDS, which for up to 16 rows

@@ -596,7 +596,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
   if (row >= rows) return;
   const int tok = (int)(row / p.group);
   const int head = h * p.group + (int)(row - (int64_t)tok * p.group);
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
   uint16_t* dst = p.out + (s.q0 + tok) * p.o_st + head * p.o_sh;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
@@ -615,7 +615,7 @@ __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(Pr
     }
   if (p.lse && ln < 32 && part == 0)
     p.lse[(int64_t)(s.q0 + tok) * p.hq + head] =
-        l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+        l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 }  // namespace

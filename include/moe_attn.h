@@ -26,7 +26,9 @@
  *    does with a value outside its range is stated there.
  *  - Scores, softmax sums, outputs and rotations are accumulated in fp32;
  *    the softmax weights are rounded to bf16 for the product with v.
- *  - Inputs that some row of the sequence keeps must be finite.  Cache slots past a sequence's
+ *  - Keys and values that some row of the sequence keeps must be finite; a
+ *    query with a NaN (such as one of a position outside the rotation table) gives
+ *    NaN in its own row of out and lse and in no other.  Cache slots past a sequence's
  *    length, keys outside every row's window and rows of other sequences
  *    are not read into any result, whatever they hold.
  *  - No call allocates device memory, clears memory by a memset, or

@@ -261,3 +261,29 @@ def test_prefill_of_more_tiles_than_a_launch_takes():
     assert torch.equal(out, x)
     del out, x
     torch.cuda.empty_cache()
+
+
+def test_rows_of_nan_are_not_empty_rows():
+    # lse is -inf for a row that keeps nothing, and NaN like the output for one whose query is NaN
+    rng = np.random.default_rng(74)
+    nan = float("nan")
+    for lens, hq, dim in (([40, 0, 300], 3, 128), ([9000, 0, 8000], 3, 64), ([700, 0, 70], 20, 128),
+                          ([3000, 0, 70], 64, 512)):       # whole, joined, many rows, many rows joined
+        p = _Paged(rng, lens, 1, dim, 16)
+        q = dev_bf16(_vals(rng, 3, hq, dim))
+        want, want_lse = moe.attn_decode(q, p.cache, dev(p.table), dev(p.lens), want_lse=True)
+        q[:2, 1] = nan
+        out, lse = moe.attn_decode(q, p.cache, dev(p.table), dev(p.lens), want_lse=True)
+        assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+        assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+        keep = [h for h in range(hq) if h != 1]
+        assert torch.equal(out[0, keep], want[0, keep]) and torch.equal(lse[0, keep], want_lse[0, keep])
+        assert torch.equal(out[2], want[2])
+    for dim in (64, 128, 256, 512):
+        q, k = dev_bf16(_vals(rng, 90, 2, dim)), dev_bf16(_vals(rng, 60, 1, dim))
+        cu_q, cu_k = dev(_cu([40, 50])), dev(_cu([40, 20]))
+        q[[7, 45], 1] = nan                                 # a row with keys, and one without
+        out, lse = moe.attn_prefill(q, k, k, cu_q, cu_k, want_lse=True)
+        assert out[7, 1].isnan().all() and lse[7, 1].isnan()
+        assert (out[40:70] == 0).all() and torch.isneginf(lse[40:70]).all()
+        assert lse.isnan().sum() == 1 and out.isnan().sum() == dim
