@@ -5,7 +5,8 @@ over the cache, and attention over packed prompts.
 Rows are bf16 tensors [tokens, heads, head_dim] whose last index is
 contiguous; the other strides are free (multiples of 8 elements), so slices of
 a fused projection's output are taken as they are.  Tensors are checked, and
-outputs made, by the binding's native half (csrc/attn_binding.cpp).
+outputs made, by the binding's native half (csrc/attn_binding.cpp).  There is no
+backward pass: rows that require a gradient are refused unless gradients are off.
 """
 
 import ctypes

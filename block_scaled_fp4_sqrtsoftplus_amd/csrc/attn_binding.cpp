@@ -10,6 +10,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -60,6 +61,9 @@ moe_rows rows(const at::Tensor& t, int64_t tokens, int64_t heads, int64_t dim, i
                      shape_text({tokens >= 0 ? tokens : s[0], heads >= 0 ? heads : s[1], dim}));
   same_device(t, index, name);
   if (s[2] > 1 && t.stride(2) != 1) refuse(name, "must be contiguous in its last index");
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse(name, "requires a gradient, which these operators do not pass on: detach it or call "
+                 "under torch.no_grad()");
   // strides over indices of one value are free
   return moe_rows{static_cast<uint16_t*>(t.data_ptr()), s[0] > 1 ? t.stride(0) : 0,
                   s[1] > 1 ? t.stride(1) : 0};

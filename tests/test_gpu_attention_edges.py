@@ -287,3 +287,24 @@ def test_rows_of_nan_are_not_empty_rows():
         assert out[7, 1].isnan().all() and lse[7, 1].isnan()
         assert (out[40:70] == 0).all() and torch.isneginf(lse[40:70]).all()
         assert lse.isnan().sum() == 1 and out.isnan().sum() == dim
+
+
+def test_inputs_that_require_gradients_are_refused():
+    # there is no backward pass: outputs without a graph would lose the gradient silently
+    cache = moe.KVCache.empty(2, 16, 2, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    y = x.clone().requires_grad_()
+    slots, table, ones, cu = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros((1, 1), **i32), \
+        torch.ones(1, **i32), torch.tensor([0, 1], **i32)
+    calls = [lambda t: moe.kv_append(cache, t, x, slots), lambda t: moe.kv_append(cache, x, t, slots),
+             lambda t: moe.kv_append(cache, x, x, slots, q=t), lambda t: moe.attn_decode(t, cache, table, ones),
+             lambda t: moe.attn_decode(x, cache, table, ones, out=t), lambda t: moe.attn_prefill(t, x, x, cu),
+             lambda t: moe.attn_prefill(x, t, t, cu), lambda t: moe.attn_prefill(x, x, t, cu)]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call(y)
+        call(x)
+        with torch.no_grad():
+            call(y)
+    torch.cuda.synchronize()
