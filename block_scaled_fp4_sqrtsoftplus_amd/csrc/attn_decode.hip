@@ -37,12 +37,17 @@ namespace moe {
 
 namespace {
 
-// Pieces the work is cut into: two workgroups a CU for the kernel without LDS
+// Pieces the work is cut into, over all heads and row groups: two workgroups a CU for the kernel without LDS
 // (of 256, 512, 768 and 1024 pieces the best or within 1% of it for 64 ragged
-// sequences, one long one and 256-element heads; 1024 take 3% and 10% more on the first two).  The one with LDS has one
-// workgroup a CU, and its own cut adds up to a piece per sequence: together
-// they stay below the CUs, since the kernel has a second round otherwise (69 instead
-// of 48 us at 32 sequences on one 512-element head).
+// sequences, one long one and 256-element heads; 1024 take 3% and 10% more on the first two).  The one with LDS cuts
+// each sequence by itself, which adds up to a piece per sequence, head and row
+// group.  With one head and row group the pieces make room for those, so that all
+// stay below the CUs of a kernel with one workgroup on each (69 instead
+// of 48 us at 32 sequences on one 512-element head without).  With several heads or row groups
+// they do not: room for a piece of each makes pieces longer and was slower, though the
+// workgroups pass 256 without it.  Four new tokens on one 512-element head, 32 ragged sequences 127 us
+// and 132 with the room; two heads of 512 99 and 105; four new tokens on 4 heads of 128 61 and 78; 256 elements 47 and
+// 49; eight heads of 512 alone gained, 195 and 182.
 constexpr int kPieces = 512;
 int pieces_rows(int batch) { return std::max(256 - batch, 128); }
 
