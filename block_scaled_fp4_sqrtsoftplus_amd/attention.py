@@ -205,7 +205,7 @@ class DecodeAttention:
 
     def __call__(self, q, block_table, seq_lens, out=None, want_lse=False):
         """q [batch * q_len, heads_q, head_dim] bf16, block_table [batch, width]
-        int32, seq_lens [batch] int32 (new tokens included): out like q, and
+        int32 contiguous, seq_lens [batch] int32 (new tokens included): out like q, and
         with want_lse also lse [batch * q_len, heads_q] fp32."""
         index = self._index
         stream = _raw_stream(index)

@@ -26,7 +26,7 @@
 // Bound by the reads of K and V, each row once.  Measured: 64 sequences of up to
 // 4096 keys, 8 heads of 128 in bf16 106 us (6.1 TB/s; the join kernel takes 4.5 of
 // them); one sequence of 131071 keys in FP8 49 us (5.5 TB/s); 32 sequences of up to 4096
-// keys, 64 query heads on one 512-element head that is keys and values 46 us
+// keys, 64 query heads on one 512-element head that is keys and values 47 us
 // (2.2 TB/s: 35 and a join of 7.6, with 31 MB of partial results between
 // them); 300 keys of 8 heads 7.8 us, a chain of latencies.
 #include <algorithm>
@@ -41,7 +41,7 @@ namespace {
 // (of 256, 512, 768 and 1024 pieces the best or within 1% of it for 64 ragged
 // sequences, one long one and 256-element heads; 1024 take 3% and 10% more on the first two).  The one with LDS cuts
 // each sequence by itself, which adds up to a piece per sequence, head and row
-// group.  With one head and row group the pieces make room for those, so that all
+// group.  With one head and row group the pieces make room for those (of up to 128 sequences), so that all
 // stay below the CUs of a kernel with one workgroup on each (69 instead
 // of 48 us at 32 sequences on one 512-element head without).  With several heads or row groups
 // they do not: room for a piece of each makes pieces longer and was slower, though the

@@ -19,12 +19,17 @@
 // few tokens: short prompts fill their tiles and little is computed above the
 // diagonal.
 //
+// P is rounded to bf16 as v is, its sum taken before: outputs are 2.0e-3 from the
+// exact ones in the 2-norm, of which their own rounding is 1.6e-3.  P as the sum of
+// two bf16 values would be a second product with V, half as many matrix
+// instructions again where they are the bound.
+//
 // Measured (TFLOP/s count what the mask leaves): 8192 tokens, 32 heads of 128 on 8
-// 501 us (1098 TFLOP/s): matrix units busy for 58% of the cycles at a clock that the load
+// 502 to 519 us (1094 to 1060 TFLOP/s): matrix units busy for 58% of the cycles at a clock that the load
 // brings down to 1.6 to 1.8 GHz, no LDS bank conflict; where the exponentials
-// and loads stand between the products makes no difference there any more.  Six packed prompts 75 us
-// (731), 2048 tokens of 64 heads on one 512-element head that is keys and
-// values 302 us (910), 200 tokens of 16 heads of 64 7.6 us, all latencies.
+// and loads stand between the products makes no difference there any more.  Six packed prompts 77 us
+// (708), 2048 tokens of 64 heads on one 512-element head that is keys and
+// values 304 us (903), 200 tokens of 16 heads of 64 7.6 us, all latencies.
 #include <algorithm>
 #include <type_traits>
 
@@ -120,7 +125,8 @@ __device__ __forceinline__ int v_at(int r, int c) {
 // their way while one is read (with ONE, where v is k, of the one tensor: three).
 // PIPE: a step takes the weights of its scores while the matrix units take the
 // next step's scores.  AHEAD: products by which LDS reads run ahead of their use,
-// where their order is fixed by hand.  WAVES: waves per SIMD that the registers are held to.
+// where their order is fixed by hand.  WAVES: waves per SIMD that the registers are
+// held to, where the LDS holds as many (256-element heads: 96 KB, one wave and more registers).
 template <int D, int BN, int RG, int SPLIT, int BUFS, bool PIPE, int AHEAD, int WAVES, bool ONE>
 __global__ __launch_bounds__(64 * RG * SPLIT, WAVES) void attn_prefill_kernel(PrefillArgs p) {
   constexpr int BM = 32 * RG;

@@ -14,10 +14,10 @@
 // that token's heads (q, then k, then v); few tokens split their heads over
 // more waves instead.
 //
-// Measured: 4099 tokens of 32 + 8 + 8 heads of 128 in bf16 21.3 us (4.8 TB/s read and
-// written, a large copy's rate), 16384 of them into an FP8 cache 80.5 us
-// (4.7 TB/s), 64 tokens on one 512-element FP8 head 6.1 us and one token
-// 5.3 us, of which a launch is 4.
+// Measured: 4099 tokens of 32 + 8 + 8 heads of 128 in bf16 21.4 us (4.8 TB/s read and
+// written, a large copy's rate), 16384 of them into an FP8 cache 80.6 us
+// (4.7 TB/s), 64 tokens on one 512-element FP8 head 5.9 us and one token
+// 5.0 us, of which a launch is 4.
 #include <algorithm>
 
 #include "attn_internal.h"

@@ -120,7 +120,7 @@ typedef struct moe_attn_config {
   int32_t head_dim;    /* 64, 128, 256 or 512                                */
   int32_t causal;      /* prefill: 0 or 1; decode is always causal           */
   int32_t window;      /* 0: none                                            */
-  float scale;         /* finite                                             */
+  float scale;         /* finite, not 0                                      */
 } moe_attn_config;
 
 /* Bytes of device workspace moe_attn_decode needs for `cfg`, whatever the
@@ -139,8 +139,9 @@ size_t moe_attn_workspace_size(const moe_attn_config* cfg);
  *   seq_lens     [batch] int32, new tokens included; less than 1 keeps
  *                nothing, more than table_width * page_size is that
  *   lse          [batch * q_len, heads_q] fp32 or NULL
- * The work of all sequences is cut into equal pieces on the device, whatever
- * their lengths; the order of every sum depends on the lengths alone, so equal calls give equal bits. */
+ * The work is cut into pieces on the device, which workgroups share; whether,
+ * and so the order of every sum, depends on cfg, the cache's sizes, table_width and the lengths
+ * alone, so equal calls give equal bits. */
 moe_status moe_attn_decode(const moe_attn_config* cfg, const moe_rows* q,
                            const moe_kv_cache* cache, const int32_t* block_table,
                            int32_t table_width, const int32_t* seq_lens, const moe_rows* out,
