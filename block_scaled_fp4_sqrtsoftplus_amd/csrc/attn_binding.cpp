@@ -99,6 +99,11 @@ int64_t number(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+bool truth(PyObject* o) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) throw python_error();
+  return r != 0;
+}
 template <class T>
 T* address(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
@@ -211,7 +216,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       a[9] == Py_None ? fresh({tokens, hq, dim}, at::kBFloat16, index) : tensor(a[9], "out");
   const moe_rows o = rows(out, tokens, hq, dim, index, "out");
   at::Tensor lse;
-  if (PyObject_IsTrue(a[10])) lse = fresh({tokens, hq}, at::kFloat, index);
+  if (truth(a[10])) lse = fresh({tokens, hq}, at::kFloat, index);
   if (width > INT32_MAX) return failed(MOE_ERR_BAD_SHAPE);
   const moe_status s =
       moe_attn_decode(cfg, &q, cache, table, (int32_t)width, lens, &o,
@@ -261,9 +266,9 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
       a[10] == Py_None ? fresh({tokens, hq, dim}, at::kBFloat16, index) : tensor(a[10], "out");
   const moe_rows o = rows(out, tokens, hq, dim, index, "out");
   at::Tensor lse;
-  if (PyObject_IsTrue(a[11])) lse = fresh({tokens, hq}, at::kFloat, index);
+  if (truth(a[11])) lse = fresh({tokens, hq}, at::kFloat, index);
   const moe_attn_config cfg{tokens,       keys,         (int32_t)batch, 1,
-                            (int32_t)hq,  (int32_t)hkv, (int32_t)dim,   PyObject_IsTrue(a[7]),
+                            (int32_t)hq,  (int32_t)hkv, (int32_t)dim,   truth(a[7]),
                             (int32_t)window, (float)scale};
   const moe_status s =
       moe_attn_prefill(&cfg, &q, &k, &v, cu_q, cu_k, &o,

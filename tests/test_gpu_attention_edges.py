@@ -308,3 +308,14 @@ def test_inputs_that_require_gradients_are_refused():
         with torch.no_grad():
             call(y)
     torch.cuda.synchronize()
+
+
+def test_flags_without_a_truth_value_are_refused():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache, x = moe.KVCache.empty(2, 16, 2, 64), torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    table, ones, cu, two = torch.zeros((1, 1), **i32), torch.ones(1, **i32), torch.tensor([0, 1], **i32), \
+        torch.tensor([1, 0])
+    for call in (lambda: moe.attn_decode(x, cache, table, ones, want_lse=two),
+                 lambda: moe.attn_prefill(x, x, x, cu, want_lse=two), lambda: moe.attn_prefill(x, x, x, cu, causal=two)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
