@@ -10,7 +10,10 @@ Entry points mirror the C names: quant_act, route, expert_ffn, layer
 (plus workspace_size and the Layer helper that keeps one workspace).  The
 attention operators of include/moe_attn.h are kv_append, attn_decode (and the
 DecodeAttention helper that keeps its workspace) and attn_prefill, with KVCache
-and Rope as handles on a paged cache and a rotation table.
+and Rope as handles on a paged cache and a rotation table.  Those of
+include/moe_serving.h are attn_tree (TreeAttention) with tree_masks, kv_compact,
+kv_copy_pages and the PagePool; windows with first tokens that stay visible are
+`sinks` of the attentions.
 """
 
 import ctypes
@@ -331,10 +334,13 @@ def layer(cfg: Config, x, weights, w_gate=None, bias=None, token_ids=None, share
 # it was built against.  Without it the layer works as before, and each of these names raises the
 # reason when it is used.
 _ATTENTION = ("KV_BF16", "KV_FP8", "DecodeAttention", "KVCache", "Rope", "attn_decode", "attn_prefill",
-              "attn_workspace_size", "kv_append")
+              "attn_workspace_size", "kv_append", "PagePool", "TreeAttention", "attn_tree", "kv_compact",
+              "kv_copy_pages", "tree_masks")
 try:
     from .attention import (  # noqa: E402,F401
         KV_BF16, KV_FP8, DecodeAttention, KVCache, Rope, attn_decode, attn_prefill, attn_workspace_size, kv_append)
+    from .serving import (  # noqa: E402,F401
+        PagePool, TreeAttention, attn_tree, kv_compact, kv_copy_pages, tree_masks)
 except ImportError as _why:
     _no_attention = str(_why)
 

@@ -187,46 +187,54 @@ def attn_workspace_size(batch, heads_q, heads_kv, head_dim, q_len=1):
 class DecodeAttention:
     """Holds the sizes, the cache and the workspace of moe_attn_decode and runs
     it on the current stream: attention of every sequence's newest q_len tokens
-    over the cache, which holds them already.  Calls that may overlap, on other
+    over the cache, which holds them already.  With a window the first `sinks` tokens
+    stay visible behind it (moe_attn_decode_sinks).  Calls that may overlap, on other
     streams, need an object each: they would share the workspace.  The object may go
     while calls are still running; a graph that recorded one needs it as long as it is replayed."""
 
-    def __init__(self, cache: KVCache, batch, heads_q, q_len=1, window=0, scale=None):
-        _check_fit(batch, q_len, heads_q, window)
+    _workspace_size = staticmethod(lib.moe_attn_workspace_size)
+
+    def __init__(self, cache: KVCache, batch, heads_q, q_len=1, window=0, scale=None, sinks=0):
+        _check_fit(batch, q_len, heads_q, window, sinks)
         self.cache, self.batch, self.heads_q, self.q_len = cache, batch, heads_q, q_len
-        self.tokens = batch * q_len
+        self.tokens, self.sinks = batch * q_len, sinks
         scale = cache.head_dim ** -0.5 if scale is None else scale
         self.c = MoeAttnConfigC(self.tokens, 0, batch, q_len, heads_q, cache.heads, cache.head_dim, 1, window, scale)
         self._at, self._index = ctypes.addressof(self.c), cache._index
-        self.ws_bytes = lib.moe_attn_workspace_size(_byref(self.c))
+        self.ws_bytes = self._workspace_size(_byref(self.c))
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=cache.device)
         self._ws = self.ws.data_ptr()
         self._streams = {_raw_stream(self._index)}   # those the allocator knows the workspace to be used on
+
+    def _on_stream(self):
+        """The current stream, which the workspace is kept for."""
+        stream = _raw_stream(self._index)
+        if stream not in self._streams:
+            self.ws.record_stream(torch.cuda.current_stream(self._index))
+            self._streams.add(stream)
+        return stream
 
     def __call__(self, q, block_table, seq_lens, out=None, want_lse=False):
         """q [batch * q_len, heads_q, head_dim] bf16, block_table [batch, width]
         int32 contiguous, seq_lens [batch] int32 (new tokens included): out like q, and
         with want_lse also lse [batch * q_len, heads_q] fp32."""
-        index = self._index
-        stream = _raw_stream(index)
-        if stream not in self._streams:
-            self.ws.record_stream(torch.cuda.current_stream(index))
-            self._streams.add(stream)
-        return _native.attn_decode(self._at, self.cache._at, index, stream, self._ws, self.ws_bytes, q,
-                                   block_table, seq_lens, out, want_lse)
+        return _native.attn_decode(self._at, self.cache._at, self._index, self._on_stream(), self._ws, self.ws_bytes, q,
+                                   block_table, seq_lens, out, want_lse, self.sinks)
 
 
-def attn_decode(q, cache: KVCache, block_table, seq_lens, q_len=1, window=0, scale=None, out=None, want_lse=False):
+def attn_decode(q, cache: KVCache, block_table, seq_lens, q_len=1, window=0, scale=None, out=None, want_lse=False,
+                sinks=0):
     """One call of DecodeAttention."""
-    a = DecodeAttention(cache, seq_lens.shape[0], q.shape[1], q_len, window, scale)
+    a = DecodeAttention(cache, seq_lens.shape[0], q.shape[1], q_len, window, scale, sinks)
     return a(q, block_table, seq_lens, out, want_lse)
 
 
-def attn_prefill(q, k, v, cu_q, cu_k=None, causal=True, window=0, scale=None, out=None, want_lse=False):
+def attn_prefill(q, k, v, cu_q, cu_k=None, causal=True, window=0, scale=None, out=None, want_lse=False, sinks=0):
     """Attention over packed prompts (moe_attn_prefill): q [tokens, heads_q, head_dim], k and v [tokens_kv, heads_kv,
     head_dim] bf16, cu_q and cu_k [sequences + 1] int32; returns out like q, and with want_lse also lse
-    [tokens, heads_q] fp32."""
+    [tokens, heads_q] fp32.  With a window the first `sinks` tokens stay visible behind it (moe_attn_prefill_sinks)."""
     if not q.is_cuda:
         raise ValueError("tensors passed to the HIP library must be on the GPU")
     index = q.get_device()
-    return _native.attn_prefill(index, _raw_stream(index), q, k, v, cu_q, cu_k, causal, window, scale, out, want_lse)
+    return _native.attn_prefill(index, _raw_stream(index), q, k, v, cu_q, cu_k, causal, window, scale, out, want_lse,
+                                sinks)

@@ -1,8 +1,8 @@
-// Native half of the Python binding of include/moe_attn.h: takes torch tensors
+// Native half of the Python binding of include/moe_attn.h and include/moe_serving.h: takes torch tensors
 // apart, checks them, makes the outputs and calls the C ABI.  A decode step's
 // calls are short (the launch itself takes the host about 4 us), and the same
 // checks in Python and ctypes took 6 to 9 us more.  Keyword handling and the
-// handles stay in attention.py.
+// handles stay in attention.py and serving.py.
 //
 // Host code only, built by the C++ compiler against torch's headers; the
 // kernels are in libmoe_fp4.so.
@@ -17,7 +17,7 @@
 #include <cmath>
 #include <string>
 
-#include "moe_attn.h"
+#include "moe_serving.h"
 
 namespace {
 
@@ -194,10 +194,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   BINDING_END
 }
 
-// attn_decode(config, cache, device, stream, ws, ws_bytes, q, block_table, seq_lens, out, want_lse)
-PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// attn_decode(config, cache, device, stream, ws, ws_bytes, q, block_table, seq_lens, out, want_lse, sinks)
+// and with masks behind them attn_tree
+PyObject* decode(PyObject* const* a, bool tree) {
   BINDING_TRY
-  if (!expects(n, 11)) return nullptr;
   const auto* cfg = address<const moe_attn_config>(a[0]);
   const auto* cache = address<const moe_kv_cache>(a[1]);
   const int index = (int)number(a[2]);
@@ -218,18 +218,173 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor lse;
   if (truth(a[10])) lse = fresh({tokens, hq}, at::kFloat, index);
   if (width > INT32_MAX) return failed(MOE_ERR_BAD_SHAPE);
-  const moe_status s =
-      moe_attn_decode(cfg, &q, cache, table, (int32_t)width, lens, &o,
-                      lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
+  const int32_t sinks = (int32_t)number(a[11]);   // the handle has checked that it fits
+  float* l = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+  moe_status s;
+  if (tree) {
+    const auto* masks = static_cast<const uint64_t*>(
+        ints(tensor(a[12], "masks"), at::kLong, {batch, cfg->q_len}, index, "masks"));
+    s = moe_attn_tree(cfg, sinks, &q, cache, table, (int32_t)width, lens, masks, &o, l,
                       address<void>(a[4]), (size_t)number(a[5]), stream);
+  } else {
+    s = moe_attn_decode_sinks(cfg, sinks, &q, cache, table, (int32_t)width, lens, &o, l,
+                              address<void>(a[4]), (size_t)number(a[5]), stream);
+  }
   return s == MOE_OK ? results(out, lse) : failed(s);
   BINDING_END
 }
+PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return expects(n, 12) ? decode(a, false) : nullptr;
+}
+PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return expects(n, 13) ? decode(a, true) : nullptr;
+}
 
-// attn_prefill(device, stream, q, k, v, cu_q, cu_k, causal, window, scale or None, out, want_lse)
+// tree_masks(device, stream, parents) -> masks, depths
+PyObject* tree_masks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BINDING_TRY
+  if (!expects(n, 3)) return nullptr;
+  const int index = (int)number(a[0]);
+  const OnDevice on(index);
+  const at::Tensor& pt = tensor(a[2], "parents");
+  if (pt.dim() != 2) throw Refused{"parents must be [batch, nodes]"};
+  const int64_t batch = pt.size(0), nodes = pt.size(1);
+  const auto* parents = static_cast<const int32_t*>(
+      ints(pt, at::kInt, {batch, nodes}, index, "parents"));
+  if (batch > INT32_MAX || nodes > INT32_MAX) return failed(MOE_ERR_BAD_SHAPE);
+  const at::Tensor masks = fresh({batch, nodes}, at::kLong, index);
+  const at::Tensor depths = fresh({batch, nodes}, at::kInt, index);
+  const moe_status s = moe_tree_masks((int32_t)batch, (int32_t)nodes, parents,
+                                      static_cast<uint64_t*>(masks.data_ptr()),
+                                      static_cast<int32_t*>(depths.data_ptr()),
+                                      address<void>(a[1]));
+  return s == MOE_OK ? results(masks, depths) : failed(s);
+  BINDING_END
+}
+
+// kv_compact(cache, device, stream, block_table, context_lens, path, counts)
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BINDING_TRY
+  if (!expects(n, 7)) return nullptr;
+  const auto* cache = address<const moe_kv_cache>(a[0]);
+  const int index = (int)number(a[1]);
+  const OnDevice on(index);
+  const at::Tensor &tt = tensor(a[3], "block_table"), &pt = tensor(a[5], "path");
+  if (tt.dim() != 2) throw Refused{"block_table must be [batch, width]"};
+  const int64_t batch = tt.size(0), width = tt.size(1);
+  if (pt.dim() != 2) throw Refused{"path must be [batch, nodes]"};
+  const int64_t nodes = pt.size(1);
+  const auto* table =
+      static_cast<const int32_t*>(ints(tt, at::kInt, {batch, width}, index, "block_table"));
+  const auto* lens = static_cast<const int32_t*>(
+      ints(tensor(a[4], "context_lens"), at::kInt, {batch}, index, "context_lens"));
+  const auto* path =
+      static_cast<const int32_t*>(ints(pt, at::kInt, {batch, nodes}, index, "path"));
+  const auto* counts = static_cast<const int32_t*>(
+      ints(tensor(a[6], "counts"), at::kInt, {batch}, index, "counts"));
+  if (batch > INT32_MAX || width > INT32_MAX || nodes > INT32_MAX) return failed(MOE_ERR_BAD_SHAPE);
+  const moe_status s = moe_kv_compact(cache, (int32_t)batch, (int32_t)nodes, table, (int32_t)width,
+                                      lens, path, counts, address<void>(a[2]));
+  if (s != MOE_OK) return failed(s);
+  Py_RETURN_NONE;
+  BINDING_END
+}
+
+// kv_copy_pages(cache, device, stream, src, dst)
+PyObject* kv_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BINDING_TRY
+  if (!expects(n, 5)) return nullptr;
+  const auto* cache = address<const moe_kv_cache>(a[0]);
+  const int index = (int)number(a[1]);
+  const OnDevice on(index);
+  const at::Tensor& st = tensor(a[3], "src");
+  if (st.dim() != 1) throw Refused{"src must be [pairs]"};
+  const int64_t pairs = st.size(0);
+  const auto* src = static_cast<const int32_t*>(ints(st, at::kInt, {pairs}, index, "src"));
+  const auto* dst =
+      static_cast<const int32_t*>(ints(tensor(a[4], "dst"), at::kInt, {pairs}, index, "dst"));
+  const moe_status s = moe_kv_copy_pages(cache, pairs, src, dst, address<void>(a[2]));
+  if (s != MOE_OK) return failed(s);
+  Py_RETURN_NONE;
+  BINDING_END
+}
+
+// pool_grow(pool, device, stream, ws, ws_bytes, cu, tokens, missing) -> slots, positions, src, dst
+PyObject* pool_grow(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BINDING_TRY
+  if (!expects(n, 8)) return nullptr;
+  const auto* pool = address<const moe_page_pool>(a[0]);
+  const int index = (int)number(a[1]);
+  const OnDevice on(index);
+  const int64_t batch = pool->batch, tokens = number(a[6]);
+  if (tokens < 0 || tokens > INT32_MAX) return failed(MOE_ERR_BAD_SHAPE);
+  const auto* cu = static_cast<const int32_t*>(
+      ints(tensor(a[5], "cu"), at::kInt, {batch + 1}, index, "cu"));
+  const at::Tensor slots = fresh({tokens}, at::kLong, index);
+  const at::Tensor positions = fresh({tokens}, at::kInt, index);
+  const at::Tensor src = fresh({batch}, at::kInt, index), dst = fresh({batch}, at::kInt, index);
+  const moe_status s =
+      moe_pool_grow(pool, tokens, cu, static_cast<int64_t*>(slots.data_ptr()),
+                    static_cast<int32_t*>(positions.data_ptr()),
+                    static_cast<int32_t*>(src.data_ptr()), static_cast<int32_t*>(dst.data_ptr()),
+                    address<int32_t>(a[7]), address<void>(a[3]), (size_t)number(a[4]),
+                    address<void>(a[2]));
+  if (s != MOE_OK) return failed(s);
+  PyObject* t = PyTuple_New(4);
+  if (!t) return nullptr;
+  const at::Tensor* all[] = {&slots, &positions, &src, &dst};
+  for (int i = 0; i < 4; ++i) {
+    PyObject* x = THPVariable_Wrap(*all[i]);
+    if (!x) {
+      Py_DECREF(t);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(t, i, x);
+  }
+  return t;
+  BINDING_END
+}
+
+// pool_fork(pool, device, stream, parents)
+PyObject* pool_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BINDING_TRY
+  if (!expects(n, 4)) return nullptr;
+  const auto* pool = address<const moe_page_pool>(a[0]);
+  const int index = (int)number(a[1]);
+  const OnDevice on(index);
+  const auto* parents = static_cast<const int32_t*>(
+      ints(tensor(a[3], "parents"), at::kInt, {pool->batch}, index, "parents"));
+  const moe_status s = moe_pool_fork(pool, parents, address<void>(a[2]));
+  if (s != MOE_OK) return failed(s);
+  Py_RETURN_NONE;
+  BINDING_END
+}
+
+// pool_trim(pool, device, stream, lens or None, window, sinks)
+PyObject* pool_trim(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BINDING_TRY
+  if (!expects(n, 6)) return nullptr;
+  const auto* pool = address<const moe_page_pool>(a[0]);
+  const int index = (int)number(a[1]);
+  const OnDevice on(index);
+  const int32_t* lens = nullptr;
+  if (a[3] != Py_None)
+    lens = static_cast<const int32_t*>(
+        ints(tensor(a[3], "lens"), at::kInt, {pool->batch}, index, "lens"));
+  const int64_t window = number(a[4]), sinks = number(a[5]);
+  if (window < INT32_MIN || window > INT32_MAX || sinks < INT32_MIN || sinks > INT32_MAX)
+    return failed(MOE_ERR_BAD_SHAPE);
+  const moe_status s =
+      moe_pool_trim(pool, lens, (int32_t)window, (int32_t)sinks, address<void>(a[2]));
+  if (s != MOE_OK) return failed(s);
+  Py_RETURN_NONE;
+  BINDING_END
+}
+
+// attn_prefill(device, stream, q, k, v, cu_q, cu_k, causal, window, scale or None, out, want_lse, sinks)
 PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   BINDING_TRY
-  if (!expects(n, 12)) return nullptr;
+  if (!expects(n, 13)) return nullptr;
   const int index = (int)number(a[0]);
   void* stream = address<void>(a[1]);
   const OnDevice on(index);
@@ -251,7 +406,7 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (has_cu_k)
     cu_k = static_cast<const int32_t*>(
         ints(tensor(a[6], "cu_k"), at::kInt, {batch + 1}, index, "cu_k"));
-  const int64_t window = number(a[8]);
+  const int64_t window = number(a[8]), sinks = number(a[12]);
   double scale = 0.0;
   if (a[9] == Py_None) {
     scale = 1.0 / std::sqrt((double)dim);
@@ -260,7 +415,7 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) return nullptr;
   }
   if (batch > INT32_MAX || hq > INT32_MAX || hkv > INT32_MAX || dim > INT32_MAX ||
-      window < INT32_MIN || window > INT32_MAX)
+      window < INT32_MIN || window > INT32_MAX || sinks < INT32_MIN || sinks > INT32_MAX)
     return failed(MOE_ERR_BAD_SHAPE);
   const at::Tensor out =
       a[10] == Py_None ? fresh({tokens, hq, dim}, at::kBFloat16, index) : tensor(a[10], "out");
@@ -271,8 +426,8 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             (int32_t)hq,  (int32_t)hkv, (int32_t)dim,   truth(a[7]),
                             (int32_t)window, (float)scale};
   const moe_status s =
-      moe_attn_prefill(&cfg, &q, &k, &v, cu_q, cu_k, &o,
-                       lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream);
+      moe_attn_prefill_sinks(&cfg, (int32_t)sinks, &q, &k, &v, cu_q, cu_k, &o,
+                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream);
   return s == MOE_OK ? results(out, lse) : failed(s);
   BINDING_END
 }
@@ -293,6 +448,13 @@ PyMethodDef g_methods[] = {
     {"kv_append", fast(kv_append), METH_FASTCALL, nullptr},
     {"attn_decode", fast(attn_decode), METH_FASTCALL, nullptr},
     {"attn_prefill", fast(attn_prefill), METH_FASTCALL, nullptr},
+    {"attn_tree", fast(attn_tree), METH_FASTCALL, nullptr},
+    {"tree_masks", fast(tree_masks), METH_FASTCALL, nullptr},
+    {"kv_compact", fast(kv_compact), METH_FASTCALL, nullptr},
+    {"kv_copy_pages", fast(kv_copy_pages), METH_FASTCALL, nullptr},
+    {"pool_grow", fast(pool_grow), METH_FASTCALL, nullptr},
+    {"pool_fork", fast(pool_fork), METH_FASTCALL, nullptr},
+    {"pool_trim", fast(pool_trim), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

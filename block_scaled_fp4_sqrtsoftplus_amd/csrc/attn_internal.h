@@ -1,8 +1,8 @@
-// Internal declarations of the attention sources (include/moe_attn.h): vector
+// Internal declarations of the attention sources (include/moe_attn.h, include/moe_serving.h): vector
 // types, small device helpers and the kernel launchers.
 #pragma once
 
-#include "moe_attn.h"
+#include "moe_serving.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -132,8 +132,34 @@ hipError_t launch_attn_decode(const moe_attn_config& c, const moe_rows& q, const
                               const int32_t* table, int table_width, const int32_t* seq_lens,
                               const moe_rows& out, float* lse, void* ws, hipStream_t st);
 
+hipError_t launch_attn_prefill_sinks(const moe_attn_config& c, int sinks, const moe_rows& q,
+                                     const moe_rows& k, const moe_rows& v, const int32_t* cu_q,
+                                     const int32_t* cu_k, const moe_rows& out, float* lse,
+                                     hipStream_t st);
+
 hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, const moe_rows& k,
                                const moe_rows& v, const int32_t* cu_q, const int32_t* cu_k,
                                const moe_rows& out, float* lse, hipStream_t st);
+
+hipError_t launch_attn_tree(const moe_attn_config& c, int sinks, const moe_rows& q,
+                            const moe_kv_cache& kv, const int32_t* table, int table_width,
+                            const int32_t* lens, const uint64_t* masks, const moe_rows& out,
+                            float* lse, void* ws, hipStream_t st);
+hipError_t launch_tree_masks(int batch, int nodes, const int32_t* parents, uint64_t* masks,
+                             int32_t* depths, hipStream_t st);
+
+hipError_t launch_kv_compact(const moe_kv_cache& c, int batch, int nodes, const int32_t* table,
+                             int width, const int32_t* lens, const int32_t* path,
+                             const int32_t* counts, hipStream_t st);
+hipError_t launch_kv_copy_pages(const moe_kv_cache& c, int64_t n, const int32_t* src,
+                                const int32_t* dst, hipStream_t st);
+
+size_t pool_ws_bytes(const moe_page_pool& p);
+hipError_t launch_pool_grow(const moe_page_pool& pool, int64_t tokens, const int32_t* cu,
+                            int64_t* slots, int32_t* positions, int32_t* src, int32_t* dst,
+                            int32_t* missing, void* ws, hipStream_t st);
+hipError_t launch_pool_fork(const moe_page_pool& pool, const int32_t* parents, hipStream_t st);
+hipError_t launch_pool_trim(const moe_page_pool& pool, const int32_t* lens, int window, int sinks,
+                            hipStream_t st);
 
 }  // namespace moe

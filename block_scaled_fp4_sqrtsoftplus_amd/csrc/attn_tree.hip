@@ -1,0 +1,60 @@
+// Attention of new tokens over the paged cache whose rows do not see all that
+// is before them (include/moe_serving.h): a tree of drafted tokens
+// (moe_attn_tree), and a window behind which the first tokens stay visible
+// (moe_attn_decode_sinks).
+//
+// Mathematics and matrix form are those of attn_decode.hip.  Both are one
+// mask: a row keeps a part of the context, [row_lo, context) and the first
+// tokens, and of the up to 64 new tokens those of a bit mask (64 bits, one
+// word a row; for rows that are causal among themselves the kernel makes it).
+#include "attn_decode_kernels.h"
+
+namespace moe {
+
+hipError_t launch_attn_tree(const moe_attn_config& c, int sinks, const moe_rows& q,
+                            const moe_kv_cache& kv, const int32_t* table, int table_width,
+                            const int32_t* lens, const uint64_t* masks, const moe_rows& out,
+                            float* lse, void* ws, hipStream_t st) {
+  return launch_decode<true>(c, q, kv, table, table_width, lens, masks, sinks, out, lse, ws, st);
+}
+
+namespace {
+
+// One wave per sequence, a node per lane.  A parent comes before its children, so
+// one turn per node hands every mask down.
+__global__ __launch_bounds__(256) void tree_masks_kernel(const int32_t* parents, uint64_t* masks,
+                                                         int32_t* depths, int batch, int nodes) {
+  const int lane = threadIdx.x & 63;
+  const int b = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (b >= batch) return;
+  const int64_t at = (int64_t)b * nodes + lane;
+  const int parent = lane < nodes ? parents[at] : -2;
+  const bool inner = parent >= 0 && parent < lane;
+  uint32_t lo = 0, hi = 0;
+  const uint32_t bit_lo = lane < 32 ? 1u << lane : 0u, bit_hi = lane < 32 ? 0u : 1u << (lane - 32);
+  if (parent == -1) {
+    lo = bit_lo;
+    hi = bit_hi;
+  }
+  for (int i = 0; i < nodes; ++i) {     // node i's mask is final in turn i
+    const uint32_t l = __builtin_amdgcn_readlane(lo, i), h = __builtin_amdgcn_readlane(hi, i);
+    if (inner && parent == i && (l | h)) {
+      lo = l | bit_lo;
+      hi = h | bit_hi;
+    }
+  }
+  if (lane >= nodes) return;
+  masks[at] = (uint64_t)hi << 32 | lo;
+  if (depths) depths[at] = __popc(lo) + __popc(hi) - 1;
+}
+
+}  // namespace
+
+hipError_t launch_tree_masks(int batch, int nodes, const int32_t* parents, uint64_t* masks,
+                             int32_t* depths, hipStream_t st) {
+  hipLaunchKernelGGL(tree_masks_kernel, dim3((batch + 3) / 4), dim3(256), 0, st, parents, masks,
+                     depths, batch, nodes);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,718 @@
+"""The operators of include/moe_serving.h against the oracle: tree attention and windows with first tokens within
+the bounds that test_gpu_attention derives, masks, moves and the page pool exactly."""
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import dev, dev_bf16, host
+from oracle import attention, serving
+from test_gpu_attention import _Paged, _check, _cu, _f, _vals
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("block_scaled_fp4_sqrtsoftplus_amd")
+
+
+def _parents(rng, batch, nodes, empty=0.2):
+    """Random trees; some places are empty, some by a parent that is not before them."""
+    p = np.full((batch, nodes), -2, np.int32)
+    for b in range(batch):
+        for i in range(nodes):
+            r = rng.random()
+            p[b, i] = rng.choice([-2, -7, i, i + 1, 1 << 20]) if r < empty else -1 if r < empty + 0.2 else \
+                rng.integers(max(-1, i - 4), i) if i else -1
+    return p
+
+
+def _bits(masks):
+    return np.array(masks, dtype=np.uint64).view(np.int64)
+
+
+@pytest.mark.parametrize("batch,nodes", [(1, 1), (3, 64), (5, 33), (70, 7), (257, 32), (1, 63)])
+def test_tree_masks(batch, nodes):
+    rng = np.random.default_rng(batch + nodes)
+    parents = _parents(rng, batch, nodes)
+    if batch == 3:
+        parents[1] = np.arange(nodes) - 1            # a chain of 64
+        parents[2] = -2
+    masks, depths = moe.tree_masks(dev(parents))
+    want, deep = serving.tree_masks(parents.tolist())
+    assert np.array_equal(masks.cpu().numpy(), _bits(want)) and np.array_equal(depths.cpu().numpy(), deep)
+
+
+# ----------------------------------------------------------------------------
+# Tree attention
+# ----------------------------------------------------------------------------
+
+
+def _tree_reference(p, q, contexts, masks, scale, window=0, sinks=0):
+    n, parts = len(masks[0]), []
+    cap = p.table.shape[1] * p.page
+    for b, c in enumerate(contexts):
+        keep = serving.tree_keep(masks[b], min(c, cap), n, window, sinks, cap)
+        keys = min(c + n, cap)
+        k, v = (attention.cache_rows(x, p.table[b], keys) for x in (p.k, p.v))
+        k, v = (np.nan_to_num(np.concatenate([x, np.zeros((x.shape[0], max(0, keep.shape[1] - x.shape[1]),
+                                                            x.shape[2]))], 1)) for x in (k, v))
+        parts.append(serving.attend(_f(q[b * n:(b + 1) * n]), k, v, keep, scale))
+    return tuple(np.concatenate(x) for x in zip(*parts))
+
+
+def _hide_unnamed(p, contexts, masks):
+    """NaN in the drafted rows that no mask names."""
+    n, fp8 = len(masks[0]), p.cache.format == moe.KV_FP8
+    for b, c in enumerate(contexts):
+        named = 0
+        for m in masks[b]:
+            named |= m
+        for j in (j for j in range(n) if not named >> j & 1):
+            pos = c + j
+            if pos // p.page >= p.table.shape[1] or p.table[b, pos // p.page] < 0:
+                continue
+            page, row = int(p.table[b, pos // p.page]), pos % p.page
+            for x, s in ((p.cache.k, p.cache.k_scale), (p.cache.v, p.cache.v_scale)):
+                x[page, :, row] = 0x7F if fp8 else float("nan")
+                if fp8:
+                    s[page, :, row] = 255
+
+
+CONTEXTS = [1, 0, 16, 17, 31, 33, 128, 129, 700, 2]
+
+
+@pytest.mark.parametrize("hq,hkv,dim,page,nodes,window,sinks,fp8,shared,by_token", [
+    (8, 8, 128, 16, 1, 0, 0, False, False, False),
+    (32, 8, 128, 16, 4, 0, 0, False, False, True),
+    (10, 2, 64, 16, 3, 0, 0, False, False, False),
+    (10, 2, 64, 64, 3, 40, 0, True, False, False),
+    (32, 8, 128, 32, 3, 20, 5, True, False, True),
+    (16, 4, 256, 16, 4, 64, 1, False, False, False),
+    (16, 4, 256, 128, 3, 130, 33, True, False, True),
+    (8, 2, 128, 16, 7, 0, 0, False, False, False),     # 28 rows a head
+    (8, 2, 64, 32, 8, 50, 2, True, False, False),
+    (4, 2, 128, 16, 26, 0, 0, False, False, False),    # 52 rows
+    (16, 4, 128, 16, 33, 0, 0, False, False, True),    # 132 rows
+    (16, 4, 128, 64, 33, 100, 3, True, False, False),
+    (4, 2, 64, 16, 64, 0, 0, False, False, False),     # every bit of a mask
+    (10, 2, 64, 16, 63, 64, 20, True, False, False),
+    (6, 1, 256, 32, 31, 0, 0, False, False, False),
+    (8, 2, 256, 16, 40, 70, 40, True, False, False),
+    (8, 1, 256, 16, 40, 0, 0, False, True, False),
+    (64, 1, 512, 64, 3, 0, 0, False, True, False),
+    (64, 1, 512, 16, 5, 90, 2, True, True, False),
+    (5, 1, 512, 16, 16, 0, 0, False, False, False),
+    (8, 1, 512, 32, 37, 50, 8, True, False, True),
+])
+def test_attn_tree(hq, hkv, dim, page, nodes, window, sinks, fp8, shared, by_token):
+    rng = np.random.default_rng(hq + dim + page + nodes)
+    batch = len(CONTEXTS)
+    p = _Paged(rng, [c + nodes for c in CONTEXTS], hkv, dim, page, fp8, shared, by_token, width=-(-800 // page) + 2)
+    parents = _parents(rng, batch, nodes)
+    parents[4] = -2                                       # a sequence whose places are all empty
+    parents[5] = np.arange(nodes) - 1
+    masks = serving.tree_masks(parents.tolist())[0]
+    _hide_unnamed(p, CONTEXTS, masks)
+    q = _vals(rng, batch * nodes, hq, dim)
+    for b in range(batch):
+        for i in range(nodes):
+            if masks[b][i] == 0:
+                q[b * nodes + i] = rng.choice([0x7FC0, 0x7F80])     # an empty place's q is not looked at
+    scale = dim ** -0.5 * 1.5
+    d = dev(np.array(CONTEXTS, np.int32))
+    out, lse = moe.attn_tree(dev_bf16(q), p.cache, dev(p.table), d, dev(_bits(masks)), window, scale, want_lse=True,
+                             sinks=sinks)
+    torch.cuda.synchronize()
+    q = np.where(np.isfinite(_f(q)), q, 0)
+    _check(out, lse, _tree_reference(p, q, CONTEXTS, masks, scale, window, sinks), dim)
+
+
+@pytest.mark.parametrize("hq,hkv,dim,nodes,fp8,contexts", [
+    (4, 1, 64, 2, False, [5000]),                       # one sequence over all splits
+    (8, 2, 128, 2, True, [9001, 3, 0, 130]),
+    (8, 2, 128, 9, False, [3000, 40, 0, 1111]),
+    (4, 1, 128, 50, True, [2500, 64, 3]),
+    (12, 1, 512, 8, False, [1500, 700]),
+    (2, 2, 64, 5, False, [60] * 130),                   # more sequences than lanes of a wave
+])
+def test_attn_tree_splits(hq, hkv, dim, nodes, fp8, contexts):
+    rng = np.random.default_rng(len(contexts) + dim)
+    p = _Paged(rng, [c + nodes for c in contexts], hkv, dim, 16, fp8)
+    masks = serving.tree_masks(_parents(rng, len(contexts), nodes, 0.1).tolist())[0]
+    q = _vals(rng, len(contexts) * nodes, hq, dim)
+    a = moe.TreeAttention(p.cache, len(contexts), hq, nodes)
+    a.ws.fill_(0xFF)                                    # the workspace need not be cleared
+    args = dev_bf16(q), dev(p.table), dev(np.array(contexts, np.int32)), dev(_bits(masks))
+    out, lse = a(*args, want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, _tree_reference(p, q, contexts, masks, dim ** -0.5), dim)
+    again, _ = a(*args, want_lse=True)
+    assert torch.equal(out, again)                      # equal calls give equal bits
+
+
+@pytest.mark.parametrize("hq,hkv,dim,nodes", [(4, 2, 128, 6), (8, 1, 128, 40), (4, 1, 512, 20)])
+def test_attn_tree_masks_that_are_no_trees(hq, hkv, dim, nodes):
+    # rows that see later nodes, or not themselves; bits past the last node are ignored
+    rng = np.random.default_rng(nodes)
+    contexts = [100, 3, 0]
+    p = _Paged(rng, [c + nodes for c in contexts], hkv, dim, 32)
+    masks = [[int(rng.integers(0, 1 << min(nodes, 62))) for _ in range(nodes)] for _ in contexts]
+    given = [[m | (0x5 << nodes if nodes < 60 else 0) for m in row] for row in masks]
+    given[0][1] = masks[0][1] = 0
+    given[1][0], masks[1][0] = 1 << 63, 0               # no node of its own: an empty place
+    q = _vals(rng, 3 * nodes, hq, dim)
+    out, lse = moe.attn_tree(dev_bf16(q), p.cache, dev(p.table), dev(np.array(contexts, np.int32)), dev(_bits(given)),
+                             want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, _tree_reference(p, q, contexts, masks, dim ** -0.5), dim)
+
+
+@pytest.mark.parametrize("hq,hkv,dim,fp8", [(4, 2, 64, False), (8, 2, 128, True), (8, 1, 128, False), (8, 1, 512, False)])
+def test_attn_tree_values_out_of_range(hq, hkv, dim, fp8):
+    rng = np.random.default_rng(17)
+    nodes = 12
+    p = _Paged(rng, [64, 64, 64, 64, 64], hkv, dim, 16, fp8, width=4)
+    masks = serving.tree_masks([[i - 1 for i in range(nodes)]] * 5)[0]
+    masks[3] = [0] * nodes
+    q = _vals(rng, 5 * nodes, hq, dim)
+    contexts = [64, 58, -5, 30, 1000]        # nodes past the table's end; below 0 is 0; past the end is the end
+    table = p.table.copy()
+    table[2] = [p.table[2, 0], -1, 1 << 20, -9]
+    out, lse = moe.attn_tree(dev_bf16(q), p.cache, dev(table), dev(np.array(contexts, np.int32)), dev(_bits(masks)),
+                             want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, _tree_reference(p, q, [64, 58, 0, 30, 64], masks, dim ** -0.5), dim)
+    gone = torch.full_like(dev(table), -1)
+    out, lse = moe.attn_tree(dev_bf16(q), p.cache, gone, dev(np.array(contexts, np.int32)), dev(_bits(masks)), want_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_attn_tree_of_a_chain_is_decode():
+    # the same keys, rows and order of sums
+    rng = np.random.default_rng(3)
+    for hq, dim, n in ((8, 128, 4), (24, 64, 3), (16, 512, 2)):
+        lens = [300, 17, 4]
+        p = _Paged(rng, lens, 1, dim, 16)
+        q = dev_bf16(_vals(rng, 3 * n, hq, dim))
+        masks, _ = moe.tree_masks(torch.arange(-1, n - 1, dtype=torch.int32, device="cuda").expand(3, n).contiguous())
+        a, la = moe.attn_tree(q, p.cache, dev(p.table), dev(p.lens - n), masks, want_lse=True)
+        b, lb = moe.attn_decode(q, p.cache, dev(p.table), dev(p.lens), n, want_lse=True)
+        # two results within test_gpu_attention's bound of the exact one
+        tol = 2 * (2.0 ** -8 * 1.01 * (a.abs().float() + _f(host(p.cache.v.nan_to_num()))[..., :].__abs__().max()))
+        assert ((a.float() - b.float()).abs() <= tol).all() and (la - lb).abs().max() < 1e-4
+
+
+# ----------------------------------------------------------------------------
+# Windows with first tokens
+# ----------------------------------------------------------------------------
+
+
+def _hidden_between(p, lens, q_len, window, sinks, free):
+    """NaN in the cache rows that no row keeps; whole pages of them out of the table."""
+    fp8, table = p.cache.format == moe.KV_FP8, p.table.copy()
+    for b, n in enumerate(lens):
+        at = np.arange(min(sinks, n), max(min(sinks, n), n - q_len + 1 - window))
+        for x, s in ((p.cache.k, p.cache.k_scale), (p.cache.v, p.cache.v_scale)):
+            if len(at):
+                pages, rows = dev(p.table[b, at // p.page].astype(np.int64)), dev((at % p.page).astype(np.int64))
+                x[pages, :, rows] = 0x7F if fp8 else float("nan")
+                if fp8:
+                    s[pages, :, rows] = 255
+        for c in range(-(-n // p.page)):
+            if free and len(at) and c * p.page >= at[0] and (c + 1) * p.page <= at[-1] + 1:
+                table[b, c] = -1 if c % 3 else 1 << 30
+    return table
+
+
+SINK_LENS = [1, 0, 16, 47, 64, 129, 200, 700, 2, 333]
+
+
+@pytest.mark.parametrize("hq,hkv,dim,page,q_len,window,sinks,fp8,shared,by_token", [
+    (8, 8, 128, 16, 1, 40, 4, False, False, False),
+    (32, 8, 128, 16, 1, 1, 1, False, False, True),
+    (10, 2, 64, 64, 3, 33, 70, True, False, False),
+    (10, 2, 64, 16, 3, 2, 3, False, False, False),         # a window inside the new tokens
+    (28, 4, 128, 32, 1, 100, 64, True, False, False),
+    (16, 4, 256, 16, 2, 64, 16, False, False, False),
+    (16, 4, 256, 128, 1, 130, 31, True, False, True),
+    (24, 1, 64, 16, 1, 31, 33, False, False, False),       # two row tiles
+    (20, 1, 128, 32, 3, 100, 2, False, False, False),      # four
+    (20, 1, 128, 32, 3, 100, 5, True, False, False),
+    (64, 1, 512, 64, 1, 96, 4, False, True, False),
+    (64, 1, 512, 16, 2, 33, 32, True, True, False),
+    (5, 1, 512, 16, 16, 5, 10, False, False, False),       # more new tokens than some sequences hold
+    (8, 2, 128, 16, 1, 1000, 4, False, False, False),      # a window longer than all
+    (8, 2, 128, 16, 2, 20, 5000, False, False, False),     # all are first tokens
+])
+def test_attn_decode_sinks(hq, hkv, dim, page, q_len, window, sinks, fp8, shared, by_token):
+    rng = np.random.default_rng(hq + dim + page + sinks)
+    p = _Paged(rng, SINK_LENS, hkv, dim, page, fp8, shared, by_token, width=-(-700 // page) + 2)
+    table = _hidden_between(p, SINK_LENS, q_len, window, sinks, True)
+    q = _vals(rng, len(SINK_LENS) * q_len, hq, dim)
+    scale = dim ** -0.5 * 1.5
+    out, lse = moe.attn_decode(dev_bf16(q), p.cache, dev(table), dev(p.lens), q_len, window, scale, want_lse=True,
+                               sinks=sinks)
+    torch.cuda.synchronize()
+    parts = []
+    for b, n in enumerate(SINK_LENS):
+        rows = [attention.cache_rows(x, p.table[b], n) for x in (p.k, p.v)]
+        parts.append(serving.attend(_f(q[b * q_len:(b + 1) * q_len]), *rows,
+                                    serving.window_keep(q_len, n, window, sinks), scale))
+    _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)
+
+
+@pytest.mark.parametrize("hq,hkv,dim,fp8,window,sinks", [
+    (4, 1, 128, False, 3000, 100), (8, 2, 128, True, 4100, 1), (24, 1, 64, False, 2000, 40),
+    (16, 1, 512, False, 1000, 129)])
+def test_attn_decode_sinks_of_long_streams(hq, hkv, dim, fp8, window, sinks):
+    # windows that are cut, far from the sequence's start
+    rng = np.random.default_rng(window)
+    page, lens = 64, [9000, 5000, 130, 20001]
+    seen = [[c for c in range(-(-n // page)) if c * page < sinks or (c + 1) * page > n - window] for n in lens]
+    short = _Paged(rng, [len(s) * page for s in seen], hkv, dim, page, fp8)
+    table = np.full((4, -(-max(lens) // page)), -1, np.int32)
+    for b, s in enumerate(seen):
+        table[b, s] = short.table[b, :len(s)]
+    q = _vals(rng, 4, hq, dim)
+    a = moe.DecodeAttention(short.cache, 4, hq, window=window, sinks=sinks)
+    a.ws.fill_(0xFF)
+    out, lse = a(dev_bf16(q), dev(table), dev(np.array(lens, np.int32)), want_lse=True)
+    torch.cuda.synchronize()
+    parts = []
+    for b, n in enumerate(lens):
+        pos = np.concatenate([np.arange(c * page, (c + 1) * page) for c in seen[b]])
+        keep = ((pos < n) & ((pos > n - 1 - window) | (pos < sinks)))[None]
+        rows = [attention.cache_rows(x, short.table[b], len(pos)) for x in (short.k, short.v)]
+        parts.append(serving.attend(_f(q[b:b + 1]), *rows, keep, dim ** -0.5))
+    _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)
+    again, _ = a(dev_bf16(q), dev(table), dev(np.array(lens, np.int32)), want_lse=True)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,dim,q_lens,k_lens,window,sinks,shared", [
+    (2, 2, 64, [1], None, 3, 1, False),
+    (2, 1, 64, [0, 130, 1, 0, 333], None, 40, 5, False),
+    (8, 2, 128, [265, 7, 400], None, 64, 64, False),
+    (8, 8, 128, [300, 164], None, 50, 3, False),
+    (6, 2, 128, [40, 129, 3], [700, 329, 3], 70, 4, False),      # a context before the prompt
+    (6, 2, 128, [40, 129], [500, 250], 1, 130, False),
+    (6, 2, 128, [140, 29], [500, 250], 33, 5000, False),         # all are first tokens
+    (4, 4, 64, [50, 220, 5], [20, 200, 0], 9, 2, False),         # fewer keys: rows that keep nothing
+    (4, 2, 256, [300, 31], [390, 531], 20, 33, False),
+    (4, 2, 256, [512], None, 100, 100, False),
+    (64, 1, 512, [5, 140], [5, 400], 60, 4, True),
+    (3, 1, 512, [250, 1], [350, 270], 31, 70, False),
+    (5, 1, 128, [1500], None, 300, 10, False),                   # many whole tiles between partly filled ones
+    (16, 1, 256, [700], None, 160, 96, False),
+])
+def test_attn_prefill_sinks(hq, hkv, dim, q_lens, k_lens, window, sinks, shared, causal):
+    rng = np.random.default_rng(hq * 3 + dim + sum(q_lens))
+    T, kl = sum(q_lens), q_lens if k_lens is None else k_lens
+    K = sum(kl)
+    kinds = 1 if shared else 2
+    wide_q, wide_k = _vals(rng, T + 1, hq + 1, dim), _vals(rng, K + 1, kinds * hkv + 1, dim)
+    wide_q[T], wide_q[:, hq], wide_k[K], wide_k[:, kinds * hkv] = 0x7FC0, 0x7FC0, 0x7FC0, 0x7FC0
+    cq, ck = _cu(q_lens), _cu(kl)
+    for b, (n, m) in enumerate(zip(q_lens, kl)):
+        # keys that no row keeps, between the first ones and the first row's window
+        wide_k[ck[b] + min(sinks, m):ck[b] + max(min(sinks, m), m - n + 1 - window)] = 0x7FC0
+    qd, kvd = dev_bf16(wide_q)[:T, :hq], dev_bf16(wide_k)[:K]
+    kd = kvd[:, :hkv]
+    vd = kd if shared else kvd[:, hkv:2 * hkv]
+    scale = dim ** -0.5 * 1.3
+    back = torch.full((T + 1, hq, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = moe.attn_prefill(qd, kd, vd, dev(cq), None if k_lens is None else dev(ck), causal, window, scale,
+                                out=back[:T], want_lse=True, sinks=sinks)
+    torch.cuda.synchronize()
+    parts = []
+    for b, (n, m) in enumerate(zip(q_lens, kl)):
+        k = _f(wide_k[ck[b]:ck[b + 1], :hkv]).swapaxes(0, 1)
+        v = k if shared else _f(wide_k[ck[b]:ck[b + 1], hkv:2 * hkv]).swapaxes(0, 1)
+        parts.append(serving.attend(_f(wide_q[cq[b]:cq[b + 1], :hq]), k, v,
+                                    serving.window_keep(n, m, window, sinks, causal), scale))
+    _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)
+    assert (back[T] == 7.0).all()
+
+
+def test_sinks_without_a_window_change_nothing():
+    rng = np.random.default_rng(8)
+    p = _Paged(rng, [300, 40], 2, 128, 16)
+    q, table, lens = dev_bf16(_vals(rng, 2, 8, 128)), dev(p.table), dev(p.lens)
+    assert torch.equal(moe.attn_decode(q, p.cache, table, lens, sinks=9), moe.attn_decode(q, p.cache, table, lens))
+    k, cu = dev_bf16(_vals(rng, 90, 2, 128)), dev(_cu([70, 20]))
+    x = dev_bf16(_vals(rng, 90, 4, 128))
+    assert torch.equal(moe.attn_prefill(x, k, k, cu, sinks=9), moe.attn_prefill(x, k, k, cu))
+
+
+# ----------------------------------------------------------------------------
+# Moves
+# ----------------------------------------------------------------------------
+
+
+def _raw(cache):
+    """Copies of everything a cache holds, as whole numbers."""
+    out = [cache.k.clone().view(torch.uint8) if cache.format == moe.KV_FP8 else cache.k.clone().view(torch.int16)]
+    if not cache.shared:
+        out.append(cache.v.clone().view(out[0].dtype))
+    for s in {id(x): x for x in (cache.k_scale, cache.v_scale) if x is not None}.values():
+        out.append(s.clone())
+    return out
+
+
+def _same(cache, want):
+    assert all(torch.equal(a, b) for a, b in zip(_raw(cache), want))
+
+
+@pytest.mark.parametrize("hkv,dim,page,nodes,fp8,shared,by_token", [
+    (8, 128, 16, 7, False, False, False), (2, 64, 32, 64, True, False, True), (1, 512, 16, 64, False, True, False),
+    (1, 512, 64, 20, True, True, False), (4, 256, 16, 33, True, False, False), (3, 64, 16, 1, False, False, True)])
+def test_kv_compact(hkv, dim, page, nodes, fp8, shared, by_token):
+    rng = np.random.default_rng(dim + nodes)
+    contexts = [0, 5, 16, 31, 100, 61, 7]
+    p = _Paged(rng, [c + nodes for c in contexts], hkv, dim, page, fp8, shared, by_token, width=12)
+    path, counts = np.full((7, nodes), 1 << 20, np.int32), np.zeros(7, np.int32)
+    for b in range(7):
+        counts[b] = rng.integers(0, nodes + 1)
+        path[b, :counts[b]] = np.sort(rng.permutation(nodes)[:counts[b]]) if b % 2 else rng.integers(0, nodes, counts[b])
+    counts[6], path[6] = nodes + 9, np.arange(nodes)[::-1]       # more than there are; rows change places
+    if nodes > 2:
+        path[1, :3], counts[1] = [nodes, -1, 1], 3                 # outside the nodes: nothing moves
+    want = [x.clone() for x in _raw(p.cache)]
+    for b, c in enumerate(contexts):
+        moves = [(c + path[b, i], c + i) for i in range(min(counts[b], nodes)) if 0 <= path[b, i] < nodes]
+        moves = [(s, t) for s, t in moves if s < 12 * page and t < 12 * page]
+        for w, old in zip(want, _raw(p.cache)):
+            for s, t in moves:
+                w[p.table[b, t // page], :, t % page] = old[p.table[b, s // page], :, s % page]
+    moe.kv_compact(p.cache, dev(p.table), dev(np.array(contexts, np.int32)), dev(path), dev(counts))
+    torch.cuda.synchronize()
+    _same(p.cache, want)
+    # nothing is moved from or to pages that are not there, or past the table's end
+    table = dev(np.full_like(p.table, -1))
+    moe.kv_compact(p.cache, table, dev(np.array(contexts, np.int32)), dev(path), dev(counts))
+    moe.kv_compact(p.cache, dev(p.table), torch.full((7,), 12 * page, dtype=torch.int32, device="cuda"), dev(path), dev(counts))
+    moe.kv_compact(p.cache, dev(p.table), dev(np.array(contexts, np.int32)), dev(path), dev(np.full(7, -3, np.int32)))
+    torch.cuda.synchronize()
+    _same(p.cache, want)
+
+
+@pytest.mark.parametrize("hkv,dim,page,fp8,shared,by_token", [
+    (8, 128, 16, False, False, False), (2, 64, 32, True, False, True), (1, 512, 16, True, True, False),
+    (5, 64, 16, True, False, False), (3, 256, 128, False, False, True), (1, 64, 4096, False, False, False)])
+def test_kv_copy_pages(hkv, dim, page, fp8, shared, by_token):
+    rng = np.random.default_rng(dim + page)
+    p = _Paged(rng, [page] * 9, hkv, dim, page, fp8, shared, by_token)
+    pages = p.cache.pages
+    src = np.array([3, 3, -1, 0, pages, 5, 7, 2], np.int32)
+    dst = np.array([1, 4, 6, -1, 8, pages, 7, -1], np.int32)
+    want = _raw(p.cache)
+    for w in want:
+        w[1], w[4] = w[3].clone(), w[3].clone()
+    moe.kv_copy_pages(p.cache, dev(src), dev(dst))
+    moe.kv_copy_pages(p.cache, dev(src[:0]), dev(dst[:0]))
+    torch.cuda.synchronize()
+    _same(p.cache, want)
+
+
+def test_moves_take_both_scales_of_one_tensor():
+    # one tensor of codes under two arrays of scales
+    codes = torch.randint(0, 256, (6, 2, 16, 256), dtype=torch.uint8, device="cuda")
+    ks, vs = (torch.randint(0, 256, (6, 2, 16, 2), dtype=torch.uint8, device="cuda") for _ in range(2))
+    cache = moe.KVCache(codes, None, ks, vs)
+    want = [x.clone() for x in (codes, ks, vs)]
+    for w in want:
+        w[4] = w[1]
+        w[2, :, 3] = w[2, :, 9]
+    moe.kv_copy_pages(cache, dev(np.array([1], np.int32)), dev(np.array([4], np.int32)))
+    moe.kv_compact(cache, dev(np.array([[2]], np.int32)), dev(np.array([3], np.int32)), dev(np.array([[6]], np.int32)),
+                   dev(np.array([1], np.int32)))          # node 6 is not among one node
+    path = dev(np.array([[6, 0, 0, 0, 0, 0, 0]], np.int32))
+    moe.kv_compact(cache, dev(np.array([[2]], np.int32)), dev(np.array([3], np.int32)), path, dev(np.array([1], np.int32)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((codes, ks, vs), want))
+
+
+# ----------------------------------------------------------------------------
+# The pool
+# ----------------------------------------------------------------------------
+
+
+def _state(pool):
+    return pool.refs.tolist(), pool.table.tolist(), pool.lens.tolist()
+
+
+def _as_pool(o):
+    return o.refs, o.table, o.lens
+
+
+@pytest.mark.parametrize("pages,page,batch,width,seed", [
+    (40, 16, 5, 7, 0), (40, 16, 5, 7, 1), (12, 32, 4, 5, 2), (300, 64, 70, 3, 3), (20000, 16, 9, 40, 4), (1, 16, 2, 2, 5),
+    (2500, 16, 1100, 2, 6), (9, 4096, 3, 3, 7)])
+def test_pool_follows_the_oracle(pages, page, batch, width, seed):
+    rng = random.Random(seed)
+    pool, want = moe.PagePool.empty(pages, page, batch, width), serving.Pool(pages, page, batch, width)
+    pool.ws.fill_(0xFF)
+    if pages == 20000:                      # the first pages are taken, but some: free ones in several chunks
+        want.refs = [0 if i % 8191 == 5 or i > 19990 else 1 for i in range(pages)]
+        pool.refs.copy_(torch.tensor(want.refs, dtype=torch.int32))
+    short = 0
+    for _ in range(25):
+        act = rng.choice(["grow", "grow", "fork", "trim", "window"])
+        if act == "grow":
+            counts = [rng.choice([0, 1, 2, page // 2 + 1, page * 2]) for _ in range(batch)]
+            cu = dev(_cu(counts))
+            slots, positions, src, dst = pool.grow(cu, sum(counts) + 3)
+            s, pos, pairs, missing = want.grow(counts)
+            assert slots.tolist() == s + [-1] * 3 and positions.tolist() == pos + [0] * 3
+            assert list(zip(src.tolist(), dst.tolist())) == pairs and pool.missing.item() == missing
+            short += missing
+        elif act == "fork":
+            parents = [rng.choice([b, rng.randint(0, batch - 1), rng.randint(-2, batch)]) for b in range(batch)]
+            pool.fork(dev(np.array(parents, np.int32)))
+            want.fork(parents)
+        else:
+            lens = [rng.randint(-1, width * page) for _ in range(batch)] if rng.random() < 0.7 else None
+            w, k = (rng.randint(1, 3 * page), rng.randint(0, 2 * page)) if act == "window" else (0, 0)
+            pool.trim(None if lens is None else dev(np.array(lens, np.int32)), w, k)
+            want.trim(lens, w, k)
+        assert _state(pool) == tuple(_as_pool(want))
+    if pages == 1:                          # two sequences and one page
+        assert short > 0
+
+
+@pytest.mark.parametrize("batch", [3000, 20000, 65536])
+def test_pool_of_many_sequences(batch):
+    # more entries than a fork's threads hold four of, and than they hold sixteen of
+    rng = np.random.default_rng(batch)
+    pool = moe.PagePool.empty(2 * batch + 50, 16, batch, 2)
+    want = serving.Pool(2 * batch + 50, 16, batch, 2)
+    counts = rng.integers(0, 33, batch).astype(np.int32)
+    slots, positions, src, dst = pool.grow(dev(_cu(counts)), int(counts.sum()))
+    s, pos, pairs, missing = want.grow(counts.tolist())
+    assert slots.tolist() == s and positions.tolist() == pos and pool.missing.item() == missing == 0
+    assert (src == -1).all() and (dst == -1).all()
+    parents = rng.integers(-1, batch, batch).astype(np.int32)
+    pool.fork(dev(parents))
+    want.fork(parents.tolist())
+    assert _state(pool) == tuple(_as_pool(want))
+
+
+def test_pool_offsets_out_of_range_stay_in_bounds():
+    pool = moe.PagePool.empty(8, 16, 3, 4)
+    cu = dev(np.array([2, 9, 5, 1 << 30], np.int32))       # from 2; a falling one; past the tokens
+    slots, positions, _, _ = pool.grow(cu, 12)
+    assert pool.lens.tolist() == [7, 0, 7]
+    assert slots.tolist()[:2] == [-1, -1] and positions.tolist()[:2] == [0, 0]
+    pool.trim(dev(np.array([-4, 5, 99], np.int32)))
+    assert pool.lens.tolist() == [0, 0, 7] and int(pool.refs.sum()) == 1
+    none = moe.PagePool.empty(0, 16, 2, 2)
+    slots, _, _, _ = none.grow(dev(np.array([0, 1, 3], np.int32)), 3)
+    assert slots.tolist() == [-1] * 3 and none.missing.item() == 2 and none.lens.tolist() == [1, 2]
+
+
+# ----------------------------------------------------------------------------
+# Together
+# ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("hq,hkv,dim,fp8,shared", [(8, 2, 128, False, False), (4, 2, 64, True, False),
+                                                   (16, 1, 512, False, True), (20, 1, 128, True, False)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (24, 3)])
+def test_drafts_are_checked_kept_and_dropped(hq, hkv, dim, fp8, shared, window, sinks):
+    """Rounds of drafting, each with a fork now and then: what the cache then holds, attended token by token, is the
+    attention of each sequence's own accepted tokens."""
+    rng = np.random.default_rng(dim + hq + window)
+    batch, nodes, page, pages = 4, 9, 16, 60
+    kv = moe.KV_FP8 if fp8 else moe.KV_BF16
+    cache, pool = moe.KVCache.empty(pages, page, hkv, dim, kv, shared), moe.PagePool.empty(pages, page, batch, 10)
+    attend = moe.TreeAttention(cache, batch, hq, nodes, window=window, sinks=sinks)
+    history = [np.zeros((0, 2, hkv, dim), np.uint16) for _ in range(batch)]     # accepted keys and values
+    cu = dev(_cu([nodes] * batch))
+    for turn in range(7):
+        if turn in (2, 4):
+            parents = [0, 0, 1, -1] if turn == 2 else [2, 1, 2, 2]
+            pool.fork(dev(np.array(parents, np.int32)))
+            history = [history[p].copy() if p >= 0 else history[0][:0] for p in parents]
+        before = pool.lens.clone()
+        tree = dev(_parents(rng, batch, nodes, 0.1))
+        masks, depths = moe.tree_masks(tree)
+        slots, _, src, dst = pool.grow(cu, batch * nodes)
+        moe.kv_copy_pages(cache, src, dst)
+        kvs, q = _vals(rng, batch * nodes, 2, hkv, dim), _vals(rng, batch * nodes, hq, dim)
+        if shared:
+            kvs[:, 1] = kvs[:, 0]
+        d = dev_bf16(kvs)
+        moe.kv_append(cache, d[:, 0], None if shared else d[:, 1], slots)
+        out, lse = attend(dev_bf16(q), pool.table, before, masks, want_lse=True)
+        torch.cuda.synchronize()
+        bits = serving.tree_masks(tree.tolist())[0]
+        parts = []
+        for b in range(batch):
+            rows = np.concatenate([history[b], kvs[b * nodes:(b + 1) * nodes]])
+            k, v = (_f(rows[:, i]).swapaxes(0, 1) for i in range(2))
+            if fp8:
+                from test_gpu_attention import _quant_rows
+                k, v = (attention.fp8_values(*_quant_rows(x)) for x in (k, v))
+            keep = serving.tree_keep(bits[b], len(history[b]), nodes, window, sinks)
+            parts.append(serving.attend(_f(q[b * nodes:(b + 1) * nodes]), k, v, keep, dim ** -0.5))
+        _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)
+        path, counts = np.full((batch, nodes), -1, np.int32), np.zeros(batch, np.int32)
+        for b in range(batch):
+            deepest = max(bits[b], key=lambda m: bin(m).count("1"))
+            nodes_of = [i for i in range(nodes) if deepest >> i & 1][:rng.integers(0, nodes + 1)]
+            counts[b] = len(nodes_of)
+            path[b, :len(nodes_of)] = nodes_of
+            history[b] = np.concatenate([history[b], kvs[[b * nodes + i for i in nodes_of]]])
+        moe.kv_compact(cache, pool.table, before, dev(path), dev(counts))
+        pool.trim(before + dev(counts), window, sinks)
+        assert pool.lens.tolist() == [len(h) for h in history] and pool.missing.item() == 0
+        held = pool.table[pool.table >= 0].tolist()
+        assert pool.refs.tolist() == [held.count(i) for i in range(pages)]
+
+
+def test_a_captured_step_replays():
+    rng = np.random.default_rng(77)
+    batch, nodes, hq, hkv, dim, page = 3, 5, 8, 2, 128, 16
+    cache = moe.KVCache.empty(40, page, hkv, dim)
+    start = moe.PagePool.empty(40, page, batch, 6)
+    n = [30, 7, 16]
+    slots, _, _, _ = start.grow(dev(_cu(n)), sum(n))
+    kv0 = dev_bf16(_vals(rng, sum(n), 2, hkv, dim))
+    moe.kv_append(cache, kv0[:, 0], kv0[:, 1], slots)
+    start.fork(dev(np.array([0, 0, 2], np.int32)))
+    kv, q = dev_bf16(_vals(rng, batch * nodes, 2, hkv, dim)), dev_bf16(_vals(rng, batch * nodes, hq, dim))
+    tree = dev(_parents(rng, batch, nodes))
+    path = dev(np.array([[1, 3, 4, 0, 0], [2, 2, 2, 2, 2], [4, 0, 0, 0, 0]], np.int32))
+    counts, cu = dev(np.array([3, 1, 0], np.int32)), dev(_cu([nodes] * batch))
+    attend = moe.TreeAttention(cache, batch, hq, nodes)
+    pool = moe.PagePool(start.refs.clone(), start.table.clone(), start.lens.clone(), page)
+    before = torch.empty_like(pool.lens)
+    first = (start.refs, start.table, start.lens)
+
+    def step():
+        before.copy_(pool.lens)
+        masks, _ = moe.tree_masks(tree)
+        slots, positions, src, dst = pool.grow(cu, batch * nodes)
+        moe.kv_copy_pages(cache, src, dst)
+        moe.kv_append(cache, kv[:, 0], kv[:, 1], slots)
+        out, lse = attend(q, pool.table, before, masks, want_lse=True)
+        d = moe.attn_decode(q[:batch], cache, pool.table, pool.lens, 1, 9, sinks=2)
+        moe.kv_compact(cache, pool.table, before, path, counts)
+        pool.trim(before + counts)
+        return slots, positions, src, dst, out, lse, d
+
+    def reset():
+        for t, s in zip((pool.refs, pool.table, pool.lens), first):
+            t.copy_(s)
+
+    def results(r):
+        return [x.clone() for x in r] + [x.clone() for x in (cache.k, cache.v, pool.refs, pool.table, pool.lens)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                             # loads the code before the capture
+        reset()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    want = results(step())
+    reset()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for turn in range(4):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(results(got), want):
+            assert torch.equal(a, b)
+        moe.attn_decode(q[:batch], cache, pool.table, pool.lens)      # eager work between
+        torch.cuda.synchronize()
+
+
+def test_on_another_stream():
+    rng = np.random.default_rng(31)
+    p = _Paged(rng, [200, 90], 2, 128, 16)
+    q = dev_bf16(_vals(rng, 6, 8, 128))
+    masks, _ = moe.tree_masks(dev(np.array([[-1, 0, 0], [-1, -1, -2]], np.int32)))
+    ctx = dev(np.array([197, 87], np.int32))
+    want = moe.attn_tree(q, p.cache, dev(p.table), ctx, masks)
+    a, pool = moe.TreeAttention(p.cache, 2, 8, 3), moe.PagePool.empty(30, 16, 2, 3)
+    table = dev(p.table)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out = a(q, table, ctx, masks)
+        slots, _, _, _ = pool.grow(dev(np.array([0, 20, 21], np.int32)), 21)
+        pool.trim(dev(np.array([3, 1], np.int32)))
+    del a
+    s.synchronize()
+    assert torch.equal(out, want) and pool.refs.sum().item() == 2 and slots.tolist() == list(range(20)) + [32]
+
+
+# ----------------------------------------------------------------------------
+# Refusals
+# ----------------------------------------------------------------------------
+
+
+def test_refusals():
+    cache = moe.KVCache.empty(4, 16, 2, 64)
+    q = torch.zeros((6, 4, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    masks = torch.ones((2, 3), dtype=torch.int64, device="cuda")
+    a = moe.TreeAttention(cache, 2, 4, 3)
+    a(q, table, lens, masks)
+    for bad, match in ((dict(q=q[:5]), "q"), (dict(masks=masks.int()), "int64"), (dict(masks=masks[:1]), "masks"),
+                       (dict(masks=masks.cpu()), "GPU"), (dict(masks=masks.repeat(1, 2)[:, ::2]), "contiguous"),
+                       (dict(context_lens=lens.long()), "int32"), (dict(block_table=table[0]), "block_table"),
+                       (dict(q=q.clone().requires_grad_()), "gradient")):
+        with pytest.raises(ValueError, match=match):
+            a(**{**dict(q=q, block_table=table, context_lens=lens, masks=masks), **bad})
+    with pytest.raises(moe.MoeError, match="UNSUPPORTED|unsupported|not"):
+        moe.attn_tree(q, cache, table, lens, masks, window=2)
+    for sinks in (-1, (1 << 30) + 1, 1 << 32):
+        with pytest.raises(moe.MoeError):
+            moe.attn_tree(q, cache, table, lens, masks, window=4, sinks=sinks)
+        with pytest.raises(moe.MoeError):
+            moe.attn_decode(q, cache, table, lens, 3, window=4, sinks=sinks)
+        with pytest.raises(moe.MoeError):
+            moe.attn_prefill(q, q[:, :2], q[:, :2], torch.tensor([0, 6], dtype=torch.int32, device="cuda"), window=4,
+                             sinks=sinks)
+    with pytest.raises(moe.MoeError):
+        moe.TreeAttention(cache, 2, 4, 65)(torch.zeros((130, 4, 64), dtype=torch.bfloat16, device="cuda"), table, lens,
+                                           torch.ones((2, 65), dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="GPU"):
+        moe.tree_masks(torch.zeros((2, 3), dtype=torch.int32))
+    with pytest.raises(ValueError, match="int32"):
+        moe.tree_masks(masks)
+    with pytest.raises(moe.MoeError):
+        moe.tree_masks(torch.zeros((2, 65), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="path"):
+        moe.kv_compact(cache, table, lens, lens, lens)
+    with pytest.raises(ValueError, match="counts"):
+        moe.kv_compact(cache, table, lens, table, lens[:1])
+    with pytest.raises(ValueError, match="dst"):
+        moe.kv_copy_pages(cache, lens, lens[:1])
+    with pytest.raises(ValueError, match="src"):
+        moe.kv_copy_pages(cache, lens.long(), lens)
+    pool = moe.PagePool.empty(4, 16, 2, 2)
+    with pytest.raises(ValueError, match="cu"):
+        pool.grow(lens, 3)
+    with pytest.raises(moe.MoeError):
+        pool.grow(torch.zeros(3, dtype=torch.int32, device="cuda"), -1)
+    with pytest.raises(ValueError, match="parents"):
+        pool.fork(lens[:1])
+    with pytest.raises(ValueError, match="lens"):
+        pool.trim(lens.long())
+    for bad in (dict(window=-1), dict(sinks=-1), dict(window=1 << 33)):
+        with pytest.raises(moe.MoeError):
+            pool.trim(**bad)
+    for args in ((lens.long(), table, lens, 16), (lens, table, lens[:1], 16), (lens, table[:, :1], lens, 16),
+                 (lens.cpu(), table, lens, 16)):
+        with pytest.raises(ValueError):
+            moe.PagePool(*args)
+    with pytest.raises(moe.MoeError):
+        moe.PagePool(lens, table, lens, 24)

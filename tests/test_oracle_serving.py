@@ -1,0 +1,100 @@
+"""Pins of the serving oracle: known small cases, and the pool's bookkeeping against its own table."""
+
+import random
+
+import numpy as np
+import pytest
+
+from oracle import attention, serving
+
+
+def test_tree_masks_by_hand():
+    #      -1      -1
+    #      0       3
+    #     1 2      4      5: empty, 6: under the empty one, 7: no parent before it
+    masks, depths = serving.tree_masks([[-1, 0, 0, -1, 3, -2, 5, 7]])
+    assert masks == [[0b1, 0b11, 0b101, 0b1000, 0b11000, 0, 0, 0]]
+    assert depths.tolist() == [[0, 1, 1, 0, 1, -1, -1, -1]]
+
+
+def test_tree_keep_is_causal_for_a_chain():
+    rng = np.random.default_rng(0)
+    n, context = 5, 9
+    q, k, v = rng.standard_normal((n, 2, 8)), rng.standard_normal((1, 14, 8)), rng.standard_normal((1, 14, 8))
+    masks, _ = serving.tree_masks([[i - 1 for i in range(n)]])
+    for window in (0, 6):
+        got = serving.attend(q, k, v, serving.tree_keep(masks[0], context, n, window), 0.3)
+        want = attention.attend(q, k, v, context, 0.3, True, window)
+        for a, b in zip(got, want):
+            assert np.allclose(a, b, rtol=1e-12, atol=0)
+
+
+def test_window_keep_with_first_keys():
+    keep = serving.window_keep(2, 10, 3, 2)
+    assert np.flatnonzero(keep[0]).tolist() == [0, 1, 6, 7, 8]
+    assert np.flatnonzero(keep[1]).tolist() == [0, 1, 7, 8, 9]
+    assert serving.window_keep(2, 1, 3, 2).tolist() == [[False], [True]]    # the first row stands before the keys
+
+
+def test_pool_by_hand():
+    p = serving.Pool(6, 16, 3, 4)
+    slots, positions, pairs, missing = p.grow([20, 0, 0])
+    assert slots == list(range(20)) and positions == list(range(20)) and missing == 0
+    p.fork([0, 0, -1])
+    assert p.table[1][:2] == [0, 1] and p.refs == [2, 2, 0, 0, 0, 0] and p.lens == [20, 20, 0]
+    # both grow on page 1: the first keeps it
+    slots, _, pairs, _ = p.grow([1, 1, 17])
+    assert pairs == [(-1, -1), (1, 2), (-1, -1)] and slots[:2] == [1 * 16 + 4, 2 * 16 + 4]
+    assert p.table[2][:2] == [3, 4] and p.refs == [2, 1, 1, 1, 1, 0]
+    p.trim([20, 3, 0])
+    assert p.lens == [20, 3, 0] and p.refs == [2, 1, 0, 0, 0, 0]
+    # sequence 1 now grows on page 0, which sequence 0 holds and does not grow on
+    _, _, pairs, _ = p.grow([0, 1, 0])
+    assert pairs[1] == (0, 2) and p.refs == [1, 1, 1, 0, 0, 0]
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_pool_counts_are_those_of_its_table(seed):
+    rng = random.Random(seed)
+    p = serving.Pool(30, 16, 5, 6)
+    rows = {}                                             # what every slot holds: the sequence's history
+    story = [[] for _ in range(5)]
+    for turn in range(60):
+        act = rng.choice(["grow", "fork", "trim", "window"])
+        if act == "grow":
+            counts = [rng.choice([0, 1, 5, 30]) for _ in range(5)]
+            before = list(p.lens)
+            slots, _, pairs, missing = p.grow(counts)
+            for a, z in pairs:
+                for r in range(16):
+                    if a >= 0:
+                        rows[z * 16 + r] = rows.get(a * 16 + r)
+            at = 0
+            for b, c in enumerate(counts):
+                for i in range(c):
+                    token = (turn, b, i)
+                    if slots[at] >= 0:
+                        rows[slots[at]] = token
+                    if before[b] + i < p.lens[b]:
+                        story[b].append(token if slots[at] >= 0 else None)
+                    at += 1
+        elif act == "fork":
+            parents = [rng.randint(-1, 4) for _ in range(5)]
+            p.fork(parents)
+            story = [list(story[x]) if x >= 0 else [] for x in parents]
+        else:
+            lens = [rng.randint(0, 90) for _ in range(5)]
+            window = act == "window"
+            p.trim(lens, 20 if window else 0, 3)
+            story = [s[:n] for s, n in zip(story, lens)]
+            if window:
+                story = [[t if j < 16 or j // 16 >= (len(s) - 19) // 16 else None for j, t in enumerate(s)]
+                         for s in story]
+        held = [page for r in p.table for page in r if page >= 0]
+        assert p.refs == [held.count(i) for i in range(30)]
+        for b, s in enumerate(story):
+            assert len(s) == p.lens[b]
+            for j, token in enumerate(s):
+                page = p.table[b][j // 16]
+                if token is not None and page >= 0:
+                    assert rows[page * 16 + j % 16] == token
