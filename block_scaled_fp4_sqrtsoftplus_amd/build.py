@@ -19,8 +19,8 @@ BINDING = os.path.join(PKG, "_attn_binding.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.cpp", "quant_act.hip", "route.hip", "expert_gemm.hip", "expert_gemm_nv.hip", "expert_gemm_w4.hip",
            "bf16_gemm.hip", "combine.hip", "cast_fp8.hip", "attn_api.cpp", "kv_append.hip", "attn_decode.hip",
-           "attn_prefill.hip", "serving_api.cpp", "attn_tree.hip", "attn_prefill_sinks.hip", "kv_move.hip",
-           "page_pool.hip"]
+           "attn_prefill.hip", "serving_api.cpp", "attn_tree.hip", "attn_tree_rows.hip", "attn_prefill_sinks.hip",
+           "kv_move.hip", "page_pool.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

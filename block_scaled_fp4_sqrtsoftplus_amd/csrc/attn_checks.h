@@ -76,11 +76,11 @@ inline moe_status check_decode(const moe_attn_config* c, int most) {
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A decode call's arguments; lens: the sequences' lengths.
-inline moe_status check_decode_call(const moe_attn_config* cfg, int most, const moe_rows* q,
+inline moe_status check_decode_call(const moe_attn_config* cfg, bool tree, const moe_rows* q,
                                     const moe_kv_cache* cache, const int32_t* block_table,
                                     int32_t table_width, const int32_t* lens, const moe_rows* out,
                                     const float* lse, const void* ws, size_t ws_bytes) {
-  moe_status s = check_decode(cfg, most);
+  moe_status s = check_decode(cfg, tree ? 64 : 16);
   if (s != MOE_OK) return s;
   if ((s = check_cache(cache)) != MOE_OK) return s;
   if (cache->heads != cfg->heads_kv || cache->head_dim != cfg->head_dim) return MOE_ERR_BAD_SHAPE;
@@ -93,7 +93,8 @@ inline moe_status check_decode_call(const moe_attn_config* cfg, int most, const 
   if ((s = check_rows(out, used)) != MOE_OK) return s;
   if (used && (!lens || (table_width > 0 && !block_table))) return MOE_ERR_NULL_ARG;
   if (!aligned4(lens) || !aligned4(block_table) || !aligned4(lse)) return MOE_ERR_MISALIGNED;
-  if (ws_bytes < attn_decode_ws_bytes(*cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < (tree ? attn_tree_ws_bytes(*cfg) : attn_decode_ws_bytes(*cfg)))
+    return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!ws) return MOE_ERR_NULL_ARG;
   if (!aligned16(ws)) return MOE_ERR_MISALIGNED;
   return MOE_OK;

@@ -52,6 +52,8 @@ struct DecodeArgs {
   int2* meta;              // [batch] first slot, splits
   const uint64_t* masks;   // TREE: [batch][q_len], or null: rows are causal
   int sinks;               // TREE: first tokens that stay visible
+  uint32_t q_flip;         // attn_tree_rows.hip: sign bits to flip in q, where scale2 is |scale| log2(e)
+  uint32_t total;          // ... and its workgroups
 };
 
 // An entry of a table that no kernel writes, at a wave-uniform index: a scalar load.
@@ -107,9 +109,10 @@ struct Seen {
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
 }
-__device__ __forceinline__ bool bit_of(uint64_t x, int i) {   // i >= 0
+// Bit i of x, as 0 or 1; 0 past the last one, any value below 0.
+__device__ __forceinline__ uint32_t bit_of(uint64_t x, int i) {
   const uint32_t w = i < 32 ? (uint32_t)x : (uint32_t)(x >> 32);
-  return i < 64 && ((w >> (i & 31)) & 1);
+  return i < 64 ? w >> (i & 31) & 1 : 0;
 }
 __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int b, int tok,
                                         bool row_live) {
@@ -154,12 +157,14 @@ __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int
   if (!s.keeps) s.mine = 0;
   return s;
 }
-// Whether the row, or any row, keeps a key of the sequence.
+// Whether the row, or any row, keeps a key of the sequence.  Without branches: lanes differ.
 __device__ __forceinline__ bool row_keeps(const Seen& s, const Range& r, int key) {
-  return key < r.ctx ? key >= s.row_lo || key < s.row_sinks : bit_of(s.mine, key - r.ctx);
+  const uint32_t context = (uint32_t)(key >= s.row_lo) | (uint32_t)(key < s.row_sinks);
+  return (key < r.ctx ? context : bit_of(s.mine, key - r.ctx)) != 0;
 }
 __device__ __forceinline__ bool any_keeps(const Seen& s, const Range& r, int key) {
-  return key < r.ctx ? key >= s.lo || key < s.sinks : bit_of(s.any, key - r.ctx);
+  const uint32_t context = (uint32_t)(key >= s.lo) | (uint32_t)(key < s.sinks);
+  return (key < r.ctx ? context : bit_of(s.any, key - r.ctx)) != 0;
 }
 
 // The work of all sequences, laid end to end in tiles, is cut into pieces, one
@@ -1028,14 +1033,10 @@ size_t decode_ws_bytes(const moe_attn_config& c) {
   return up256(rows * c.head_dim * 4) + 2 * up256(rows * 4) + up256((size_t)c.batch * 8);
 }
 
-// masks, sinks: see DecodeArgs.
-template <bool TREE>
-hipError_t launch_decode(const moe_attn_config& c, const moe_rows& q, const moe_kv_cache& kv,
-                         const int32_t* table, int table_width, const int32_t* seq_lens,
-                         const uint64_t* masks, int sinks, const moe_rows& out, float* lse,
-                         void* ws, hipStream_t st) {
-  if (c.batch == 0) return hipSuccess;
-  const DecodePlan d = plan_of(c);
+// The arguments that do not depend on the cut of the work.
+DecodeArgs decode_args(const moe_attn_config& c, const moe_rows& q, const moe_kv_cache& kv,
+                       const int32_t* table, int table_width, const int32_t* seq_lens,
+                       const moe_rows& out, float* lse) {
   DecodeArgs a{};
   a.q = q.p; a.q_st = q.stride_token; a.q_sh = q.stride_head;
   a.out = out.p; a.o_st = out.stride_token; a.o_sh = out.stride_head;
@@ -1049,18 +1050,46 @@ hipError_t launch_decode(const moe_attn_config& c, const moe_rows& q, const moe_
   a.page_shift = __builtin_ctz((unsigned)kv.page_size);
   a.batch = c.batch; a.q_len = c.q_len; a.hq = c.heads_q; a.hkv = c.heads_kv;
   a.group = c.heads_q / c.heads_kv;
+  a.window = c.window; a.scale2 = c.scale * kLog2e;
+  return a;
+}
+
+// Keys of a sequence that its rows may reach, by the table's width and the window.
+template <bool TREE>
+int64_t longest_walk(const moe_attn_config& c, const DecodeArgs& a) {
+  const int64_t longest = (int64_t)a.table_width << a.page_shift;
+  if (!TREE || c.window == 0) return longest;
+  return std::min(longest, (int64_t)c.window + a.sinks + c.q_len + 64);
+}
+
+hipError_t launch_join(const moe_attn_config& c, DecodeArgs a, hipStream_t st) {
+#define MOE_JOIN(D) \
+  case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), grid, dim3(256), 0, st, a); break;
+  return launch_workgroups((int64_t)c.batch * c.heads_kv * a.rows, [&](uint32_t first, dim3 grid) {
+    a.first = first;
+    switch (c.head_dim) { MOE_JOIN(64) MOE_JOIN(128) MOE_JOIN(256) MOE_JOIN(512) }
+  });
+#undef MOE_JOIN
+}
+
+// masks, sinks: see DecodeArgs.
+template <bool TREE>
+hipError_t launch_decode(const moe_attn_config& c, const moe_rows& q, const moe_kv_cache& kv,
+                         const int32_t* table, int table_width, const int32_t* seq_lens,
+                         const uint64_t* masks, int sinks, const moe_rows& out, float* lse,
+                         void* ws, hipStream_t st) {
+  if (c.batch == 0) return hipSuccess;
+  const DecodePlan d = plan_of(c);
+  DecodeArgs a = decode_args(c, q, kv, table, table_width, seq_lens, out, lse);
+  a.masks = masks; a.sinks = sinks;
   a.rows = d.rows; a.rgroups = d.rgroups;
+  const int eb = kv.format == MOE_KV_FP8 ? 1 : 2;
   const bool one = kv.k == kv.v && (eb == 2 || kv.k_scale == kv.v_scale);
-  int64_t longest = (int64_t)table_width << a.page_shift;
-  if (TREE && c.window > 0)      // no more is read, however long the sequences are
-    longest = std::min(longest, (int64_t)c.window + sinks + c.q_len + 64);
   const bool whole = whole_sequences(
-      longest * c.head_dim * eb * (one ? 1 : 2),
+      longest_walk<TREE>(c, a) * c.head_dim * eb * (one ? 1 : 2),
       (int64_t)c.batch * c.heads_kv * d.rgroups, row_tiles(d.rows, c.head_dim) > 1);
   a.pieces = whole ? 0 : d.pieces;
   a.tile_shift = row_tiles(d.rows, c.head_dim) == 1 ? 7 : 6;
-  a.masks = masks; a.sinks = sinks;
-  a.window = c.window; a.scale2 = c.scale * kLog2e;
   const size_t rows = (size_t)d.slots * c.heads_kv * d.rows;
   char* w = static_cast<char*>(ws);
   a.part_o = reinterpret_cast<float*>(w); w += up256(rows * c.head_dim * 4);
@@ -1112,13 +1141,7 @@ hipError_t launch_decode(const moe_attn_config& c, const moe_rows& q, const moe_
 #undef MOE_ROWS_ANY
 #undef MOE_ROWS
   if (e != hipSuccess || whole) return e;
-#define MOE_JOIN(D) \
-  case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), grid, dim3(256), 0, st, a); break;
-  return launch_workgroups((int64_t)c.batch * c.heads_kv * d.rows, [&](uint32_t first, dim3 grid) {
-    a.first = first;
-    switch (c.head_dim) { MOE_JOIN(64) MOE_JOIN(128) MOE_JOIN(256) MOE_JOIN(512) }
-  });
-#undef MOE_JOIN
+  return launch_join(c, a, st);
 }
 
 }  // namespace

@@ -141,6 +141,15 @@ hipError_t launch_attn_prefill(const moe_attn_config& c, const moe_rows& q, cons
                                const moe_rows& v, const int32_t* cu_q, const int32_t* cu_k,
                                const moe_rows& out, float* lse, hipStream_t st);
 
+// Sets of rows for which the kernel on 32-row tiles is taken (attn_tree_rows.hip).
+bool tree_rows_apply(const moe_attn_config& c);
+size_t tree_rows_ws_bytes(const moe_attn_config& c);
+hipError_t launch_tree_rows(const moe_attn_config& c, int sinks, const moe_rows& q,
+                            const moe_kv_cache& kv, const int32_t* table, int table_width,
+                            const int32_t* lens, const uint64_t* masks, const moe_rows& out,
+                            float* lse, void* ws, hipStream_t st);
+// masks null: rows are causal among themselves, `lens` counts them (attn_decode_ws_bytes).
+size_t attn_tree_ws_bytes(const moe_attn_config& c);
 hipError_t launch_attn_tree(const moe_attn_config& c, int sinks, const moe_rows& q,
                             const moe_kv_cache& kv, const int32_t* table, int table_width,
                             const int32_t* lens, const uint64_t* masks, const moe_rows& out,

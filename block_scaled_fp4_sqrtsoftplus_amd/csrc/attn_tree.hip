@@ -11,10 +11,17 @@
 
 namespace moe {
 
+size_t attn_tree_ws_bytes(const moe_attn_config& c) {
+  return tree_rows_apply(c) ? tree_rows_ws_bytes(c) : decode_ws_bytes(c);
+}
+
 hipError_t launch_attn_tree(const moe_attn_config& c, int sinks, const moe_rows& q,
                             const moe_kv_cache& kv, const int32_t* table, int table_width,
                             const int32_t* lens, const uint64_t* masks, const moe_rows& out,
                             float* lse, void* ws, hipStream_t st) {
+  if (c.batch == 0) return hipSuccess;
+  if (masks && tree_rows_apply(c))
+    return launch_tree_rows(c, sinks, q, kv, table, table_width, lens, masks, out, lse, ws, st);
   return launch_decode<true>(c, q, kv, table, table_width, lens, masks, sinks, out, lse, ws, st);
 }
 

@@ -40,7 +40,7 @@ moe_status moe_attn_decode_sinks(const moe_attn_config* cfg, int32_t sinks, cons
                                  int32_t table_width, const int32_t* seq_lens,
                                  const moe_rows* out, float* lse, void* ws, size_t ws_bytes,
                                  void* stream) {
-  moe_status s = check_decode_call(cfg, 16, q, cache, block_table, table_width, seq_lens, out, lse,
+  moe_status s = check_decode_call(cfg, false, q, cache, block_table, table_width, seq_lens, out, lse,
                                    ws, ws_bytes);
   if (s != MOE_OK) return s;
   if (sinks < 0 || sinks > kMostTokens) return MOE_ERR_BAD_SHAPE;
@@ -84,7 +84,7 @@ moe_status moe_tree_masks(int32_t batch, int32_t nodes, const int32_t* parents, 
 }
 
 size_t moe_attn_tree_workspace_size(const moe_attn_config* cfg) {
-  return check_decode(cfg, 64) == MOE_OK ? attn_decode_ws_bytes(*cfg) : 0;
+  return check_decode(cfg, 64) == MOE_OK ? attn_tree_ws_bytes(*cfg) : 0;
 }
 
 moe_status moe_attn_tree(const moe_attn_config* cfg, int32_t sinks, const moe_rows* q,
@@ -92,7 +92,7 @@ moe_status moe_attn_tree(const moe_attn_config* cfg, int32_t sinks, const moe_ro
                          int32_t table_width, const int32_t* context_lens, const uint64_t* masks,
                          const moe_rows* out, float* lse, void* ws, size_t ws_bytes,
                          void* stream) {
-  moe_status s = check_decode_call(cfg, 64, q, cache, block_table, table_width, context_lens, out,
+  moe_status s = check_decode_call(cfg, true, q, cache, block_table, table_width, context_lens, out,
                                    lse, ws, ws_bytes);
   if (s != MOE_OK) return s;
   if (sinks < 0 || sinks > kMostTokens) return MOE_ERR_BAD_SHAPE;
