@@ -76,44 +76,57 @@ __device__ __forceinline__ bool find_cut(const DecodeArgs& p, int w, Cut& c) {
   return false;
 }
 
-// Pages of 16-key tiles of the walk, 64 in `now` and the next 64, a tile per lane.
-struct WalkPages {
+// Where 16-key tiles of the walk lie, 64 of them and the next 64, a tile per
+// lane: a step gets the places of its tiles from lanes, with no page to wait for
+// and no product to form.
+template <bool FP8>
+struct WalkTiles {
+  struct Group {
+    uint32_t lo, hi;       // byte offset of the tile's first row in k and v
+    uint32_t slo, shi;     // FP8: its row among the scales
+    uint64_t ok;           // tiles whose page is there
+  };
   const int32_t* row;
   Range rng;
-  int base, now, next;
-  uint64_t ok_now, ok_next;    // tiles whose page is there
-  __device__ __forceinline__ int load(const DecodeArgs& p, int tile) const {
-    int64_t key = 16 * ((int64_t)tile + (threadIdx.x & 63));
-    if (key >= rng.end) return -1;
-    if (key >= rng.front) key += rng.gap;
-    const int id = row[key >> p.page_shift];
-    return id >= 0 && id < p.pages ? id : -1;
+  int base, h;
+  Group now, next;
+  __device__ __forceinline__ Group load(const DecodeArgs& p, int tile) const {
+    const int64_t v = 16 * ((int64_t)tile + (threadIdx.x & 63));
+    int id = -1;
+    int64_t key = v;
+    if (v < rng.end) {
+      if (key >= rng.front) key += rng.gap;
+      id = row[key >> p.page_shift];
+    }
+    const bool ok = id >= 0 && id < p.pages;
+    const int64_t page = ok ? id : 0;
+    const int in_page = (int)(key & ((1 << p.page_shift) - 1));
+    const int64_t off = page * p.sp + h * p.sh + in_page * p.st;
+    const int64_t srow = FP8 ? ((page * p.hkv + h) << p.page_shift) + in_page : 0;
+    return Group{(uint32_t)off, (uint32_t)(off >> 32), (uint32_t)srow, (uint32_t)(srow >> 32), __ballot(ok)};
   }
-  __device__ __forceinline__ WalkPages(const DecodeArgs& p, const Range& r, int b, int tile)
-      : row(p.table + (int64_t)b * p.table_width), rng(r), base(tile) {
+  __device__ __forceinline__ WalkTiles(const DecodeArgs& p, const Range& r, int b, int head, int tile)
+      : row(p.table + (int64_t)b * p.table_width), rng(r), base(tile), h(head) {
     now = load(p, base);
     next = load(p, base + 64);
-    ok_now = __ballot(now >= 0);
-    ok_next = __ballot(next >= 0);
   }
   // no tile before this one is asked for any more
   __device__ __forceinline__ void advance(const DecodeArgs& p, int tile) {
     if (tile < base + 64) return;
     base += 64;
     now = next;
-    ok_now = ok_next;
     next = load(p, base + 64);
-    ok_next = __ballot(next >= 0);
   }
-  __device__ __forceinline__ int at(int tile) const {
+  __device__ __forceinline__ int64_t offset(int tile) const {
     const int i = tile - base;
-    return i < 64 ? __builtin_amdgcn_readlane(now, i) : __builtin_amdgcn_readlane(next, i - 64);
+    return (int64_t)(((uint64_t)__builtin_amdgcn_readlane(now.hi, i) << 32) | (uint32_t)__builtin_amdgcn_readlane(now.lo, i));
   }
-  // bits of N tiles from this one on
-  __device__ __forceinline__ uint32_t ok(int tile) const {
+  __device__ __forceinline__ int64_t scale_row(int tile) const {
     const int i = tile - base;
-    return i < 64 ? (uint32_t)(ok_now >> i) : (uint32_t)(ok_next >> (i - 64));
+    return (int64_t)(((uint64_t)__builtin_amdgcn_readlane(now.shi, i) << 32) | (uint32_t)__builtin_amdgcn_readlane(now.slo, i));
   }
+  // bits of the tiles from this one on
+  __device__ __forceinline__ uint32_t ok(int tile) const { return (uint32_t)(now.ok >> (tile - base)); }
 };
 
 // ONE: one tensor serves as keys and values, and is loaded once (512-element
@@ -178,8 +191,7 @@ __global__ __launch_bounds__(D == 512 ? 512 : 256, 2) void attn_tree_rows_kernel
   const int first = cut.tile << p.tile_shift;
   const int last = min(rng.end, first + (cut.tiles << p.tile_shift));
   const int steps = last > first ? (last - first + BN - 1) / BN : 0;
-  WalkPages pages(p, rng, cut.b, first >> 4);
-  const int page_mask = (1 << p.page_shift) - 1;
+  WalkTiles<FP8> tiles(p, rng, cut.b, h, first >> 4);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
   // Staging: chunk i of a thread lies in row r0 + RS i of the tile, whose wave's
@@ -198,26 +210,44 @@ __global__ __launch_bounds__(D == 512 ? 512 : 256, 2) void attn_tree_rows_kernel
       all = all && ((base >= seen.lo && base + 32 <= rng.ctx) || base + 32 <= seen.sinks);
     }
     constexpr uint32_t bits = (1u << (BN / 16)) - 1;
-    return all && (pages.ok(at0 >> 4) & bits) == bits;
+    return all && (tiles.ok(at0 >> 4) & bits) == bits;
   };
+  const int c_once = tid % C;
   auto chunk = [&](int t, int r) {
-    int c0 = D == 512 ? lane : tid % C;
-    asm volatile("" : "+v"(c0));              // no places kept over the loop
+    int c0 = c_once;
+    if constexpr (D >= 256) asm volatile("" : "+v"(c0));   // no places kept over the loop
     return c0 ^ (t ? v_swz<D>(r) : k_swz<D>(r));
   };
+  const int st = (int)p.st;
   auto fetch = [&](int buf, int at0) {
-    pages.advance(p, at0 >> 4);
-    const bool all = whole(at0);
+    tiles.advance(p, at0 >> 4);
+    if (whole(at0)) {
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        const int tile = (at0 + wr0 + RS * i) >> 4;     // of the wave's rows of this load
+        const int64_t off = tiles.offset(tile);
+        const int r = (r0 + RS * i) & 15;               // this lane's row of the 16
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const char* base = (t ? p.v : p.k) + off;
+          const int c = chunk(t, r0 + RS * i);
+          if constexpr (FP8) {
+            reg[t][i] = *reinterpret_cast<const u32x2*>(base + (uint32_t)(r * st + 8 * c));
+            rsc[t][i] = (t ? p.vs : p.ks)[tiles.scale_row(tile) * NG + (uint32_t)(r * NG + c / 16)];
+          } else {
+            load_lds16(lds0 + (2 * t + buf) * TB + wv * 1024 + i * TH * 16, base, (uint32_t)(r * st + 16 * c));
+          }
+        }
+      }
+      return;
+    }
+    // keys that no row keeps, and those of pages that are not there, are zeros
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const int wr = wr0 + RS * i;            // the wave's first row of this load
-      const int place = at0 + (wr & ~15);
-      const int pid = pages.at(place >> 4);
-      const int key = rng.key_of(place);      // of the 16-key tile's first row
-      const int64_t off = (int64_t)max(pid, 0) * p.sp + h * p.sh + (int64_t)(key & page_mask) * p.st;
-      const int64_t srow = (((int64_t)max(pid, 0) * p.hkv + h) << p.page_shift) + (key & page_mask);
-      const int r = (r0 + RS * i) & 15;       // this lane's row of the 16
-      const bool read = all || (pid >= 0 && any_keeps(seen, rng, key + r));
+      const int place = at0 + ((wr0 + RS * i) & ~15), tile = place >> 4;
+      const int64_t off = tiles.offset(tile);
+      const int r = (r0 + RS * i) & 15;
+      const bool read = (tiles.ok(tile) & 1) != 0 && any_keeps(seen, rng, rng.key_of(place) + r);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const char* base = (t ? p.v : p.k) + off;
@@ -226,18 +256,13 @@ __global__ __launch_bounds__(D == 512 ? 512 : 256, 2) void attn_tree_rows_kernel
           reg[t][i] = u32x2{0, 0};
           rsc[t][i] = 127;
           if (read) {
-            reg[t][i] = *reinterpret_cast<const u32x2*>(base + (uint32_t)(r * (int)p.st + 8 * c));
-            rsc[t][i] = (t ? p.vs : p.ks)[srow * NG + (uint32_t)(r * NG + c / 16)];
+            reg[t][i] = *reinterpret_cast<const u32x2*>(base + (uint32_t)(r * st + 8 * c));
+            rsc[t][i] = (t ? p.vs : p.ks)[tiles.scale_row(tile) * NG + (uint32_t)(r * NG + c / 16)];
           }
         } else {
-          const int to = (2 * t + buf) * TB + wv * 1024 + i * TH * 16;
-          if (all) {
-            load_lds16(lds0 + to, base, (uint32_t)(r * (int)p.st + 16 * c));
-          } else {
-            u32x4 x = {0, 0, 0, 0};
-            if (read) x = *reinterpret_cast<const u32x4*>(base + (uint32_t)(r * (int)p.st + 16 * c));
-            *reinterpret_cast<u32x4*>(lds + to + lane * 16) = x;
-          }
+          u32x4 x = {0, 0, 0, 0};
+          if (read) x = *reinterpret_cast<const u32x4*>(base + (uint32_t)(r * st + 16 * c));
+          *reinterpret_cast<u32x4*>(lds + (2 * t + buf) * TB + wv * 1024 + i * TH * 16 + lane * 16) = x;
         }
       }
     }
@@ -280,7 +305,7 @@ __global__ __launch_bounds__(D == 512 ? 512 : 256, 2) void attn_tree_rows_kernel
   step_barrier<0>();
   for (int it = 0; it < steps; ++it) {
     const int at0 = first + it * BN, buf = it & 1;
-    const uint32_t ok = pages.ok(at0 >> 4);   // before the pages move on
+    const uint32_t ok = tiles.ok(at0 >> 4);   // before they move on
     bool inner = (ok & ((1u << (BN / 16)) - 1)) == (1u << (BN / 16)) - 1;
 #pragma unroll
     for (int t = 0; t < NK; ++t) {
@@ -404,6 +429,45 @@ __global__ __launch_bounds__(D == 512 ? 512 : 256, 2) void attn_tree_rows_kernel
   }
 }
 
+// Joins the parts of sequences that are cut: a row per D / 4 lanes, parts one
+// after another.  There are many rows and few parts, unlike in attn_decode's join (17.6 us where this takes
+// 7.1, 26 nodes of 32 sequences).
+template <int D>
+__global__ __launch_bounds__(256) void attn_tree_join_kernel(DecodeArgs p) {
+  constexpr int GL = D / 4, ROWS = 256 / GL;
+  const uint32_t per_b = (uint32_t)(p.hkv * p.rows);
+  const uint32_t groups = (per_b + ROWS - 1) / ROWS;
+  const uint32_t wg = p.first + blockIdx.x;
+  const uint32_t b = wg / groups;
+  const int2 mt = p.meta[b];
+  if (mt.y <= 1) return;
+  const uint32_t hr = (wg - b * groups) * ROWS + threadIdx.x / GL;   // head and row
+  if (hr >= per_b) return;
+  const int gl = threadIdx.x % GL;
+  const int64_t at0 = (int64_t)mt.x * per_b + hr;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f, m = kNoMax;
+#pragma unroll 4
+  for (int i = 0; i < mt.y; ++i) {
+    const int64_t at = at0 + (int64_t)i * per_b;
+    const float mi = p.part_m[at], li = p.part_l[at];
+    const f32x4 oi = *reinterpret_cast<const f32x4*>(p.part_o + at * D + gl * 4);
+    const float mn = fmaxf(m, mi);
+    const float a = exp2_fast(m - mn), c = exp2_fast(mi - mn);
+    m = mn;
+    l = l * a + li * c;
+    o = o * a + oi * c;
+  }
+  o *= l == 0.f ? 0.f : 1.0f / l;
+  const int h = hr / p.rows, row = hr - h * p.rows;
+  const int tok = row / p.group, head = h * p.group + row - tok * p.group;
+  const int64_t qrow = (int64_t)b * p.q_len + tok;
+  *reinterpret_cast<u32x2*>(p.out + qrow * p.o_st + head * p.o_sh + gl * 4) =
+      u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+  if (p.lse && gl == 0)
+    p.lse[qrow * p.hq + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
 }  // namespace
 
 bool tree_rows_apply(const moe_attn_config& c) { return c.q_len * (c.heads_q / c.heads_kv) > 64; }
@@ -475,7 +539,14 @@ hipError_t launch_tree_rows(const moe_attn_config& c, int sinks, const moe_rows&
 #undef MOE_TREE
 #undef MOE_TREE_ROWS
   if (e != hipSuccess || !cut) return e;
-  return launch_join(c, a, st);
+#define MOE_JOIN(D) \
+  case D: hipLaunchKernelGGL((attn_tree_join_kernel<D>), grid, dim3(256), 0, st, a); break;
+  const int64_t groups = ((int64_t)c.heads_kv * a.rows * (c.head_dim / 4) + 255) / 256;   // of a sequence
+  return launch_workgroups(c.batch * groups, [&](uint32_t first, dim3 grid) {
+    a.first = first;
+    switch (c.head_dim) { MOE_JOIN(64) MOE_JOIN(128) MOE_JOIN(256) MOE_JOIN(512) }
+  });
+#undef MOE_JOIN
 }
 
 }  // namespace moe
