@@ -53,7 +53,8 @@ struct DecodeArgs {
   const uint64_t* masks;   // TREE: [batch][q_len], or null: rows are causal
   int sinks;               // TREE: first tokens that stay visible
   uint32_t q_flip;         // attn_tree_rows.hip: sign bits to flip in q, where scale2 is |scale| log2(e)
-  uint32_t total;          // ... and its workgroups
+  uint32_t total;          // ... its workgroups
+  int row_groups;          // ... and their groups of 32 rows
 };
 
 // An entry of a table that no kernel writes, at a wave-uniform index: a scalar load.
@@ -141,7 +142,8 @@ __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int
     first = min(first, __shfl_xor(first, i));
     last = max(last, __shfl_xor(last, i));
   }
-  s.any = (uint64_t)any1 << 32 | any0;
+  s.any = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(any1) << 32 |
+          (uint32_t)__builtin_amdgcn_readfirstlane(any0);
   const int at = __shfl(pos, tok);
   const int there = __shfl((int)live, tok);   // by all lanes: any may be asked
   s.keeps = row_live && there;
@@ -152,7 +154,7 @@ __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int
   s.row_sinks = s.keeps ? sinks : 0;
   const bool some = first != INT_MAX;
   s.lo = __builtin_amdgcn_readfirstlane(some ? start(first) : INT_MAX);
-  s.sinks = some ? sinks : 0;
+  s.sinks = __builtin_amdgcn_readfirstlane(some ? sinks : 0);
   s.all_lo = __builtin_amdgcn_readfirstlane(some ? start(last) : INT_MAX);
   if (!s.keeps) s.mine = 0;
   return s;
