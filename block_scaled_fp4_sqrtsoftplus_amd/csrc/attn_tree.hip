@@ -27,29 +27,31 @@ hipError_t launch_attn_tree(const moe_attn_config& c, int sinks, const moe_rows&
 
 namespace {
 
-// One wave per sequence, a node per lane.  A parent comes before its children, so
-// one turn per node hands every mask down.
+// One wave per sequence, a node per lane: in each of six turns a node takes the
+// mask of the node it points to and then points where that one does, so that after
+// them it holds up to 64 nodes and points past the chain's end.
 __global__ __launch_bounds__(256) void tree_masks_kernel(const int32_t* parents, uint64_t* masks,
                                                          int32_t* depths, int batch, int nodes) {
+  constexpr int kRoot = -1, kNone = -2;
   const int lane = threadIdx.x & 63;
   const int b = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (b >= batch) return;
   const int64_t at = (int64_t)b * nodes + lane;
-  const int parent = lane < nodes ? parents[at] : -2;
-  const bool inner = parent >= 0 && parent < lane;
-  uint32_t lo = 0, hi = 0;
-  const uint32_t bit_lo = lane < 32 ? 1u << lane : 0u, bit_hi = lane < 32 ? 0u : 1u << (lane - 32);
-  if (parent == -1) {
-    lo = bit_lo;
-    hi = bit_hi;
-  }
-  for (int i = 0; i < nodes; ++i) {     // node i's mask is final in turn i
-    const uint32_t l = __builtin_amdgcn_readlane(lo, i), h = __builtin_amdgcn_readlane(hi, i);
-    if (inner && parent == i && (l | h)) {
-      lo = l | bit_lo;
-      hi = h | bit_hi;
+  int up = lane < nodes ? parents[at] : kNone;
+  if (up >= lane || up < kRoot) up = kNone;      // a parent comes before its children
+  uint32_t lo = lane < 32 ? 1u << lane : 0u, hi = lane < 32 ? 0u : 1u << (lane - 32);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const int from = up < 0 ? lane : up;
+    const uint32_t l = __shfl(lo, from), h = __shfl(hi, from);
+    const int next = __shfl(up, from);
+    if (up >= 0) {
+      lo |= l;
+      hi |= h;
+      up = next;
     }
   }
+  if (up != kRoot) lo = hi = 0;
   if (lane >= nodes) return;
   masks[at] = (uint64_t)hi << 32 | lo;
   if (depths) depths[at] = __popc(lo) + __popc(hi) - 1;

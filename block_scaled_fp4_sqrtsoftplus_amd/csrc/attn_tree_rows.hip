@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
       return true;
     }
     // keys that no row keeps, and those of pages that are not there, are zeros
-#pragma unroll
+#pragma unroll D == 512 && !FP8 ? 1 : LD
     for (int i = 0; i < LD; ++i) {
       const int r = row_of(i), c = chunk(t, r);
       const char* base = data + pl.off[i / LPT];

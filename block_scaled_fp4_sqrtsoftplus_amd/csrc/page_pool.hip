@@ -242,6 +242,124 @@ __global__ __launch_bounds__(256) void pool_fill_kernel(GrowArgs p, uint32_t seq
   p.positions[t] = pos;
 }
 
+// All of it in one workgroup, for pools and calls of the sizes below: three launches and
+// their latencies become one (6 sequences and 4000 pages: 8 us instead of 20.5).
+constexpr int kSmallBatch = kThreads, kSmallPages = 64 * kThreads, kSmallTokens = 32 * kThreads;
+constexpr int kSmallWanted = 8192;       // pages a call may want
+constexpr int kSlots = 2 * kSmallBatch;  // places for shared pages
+
+__global__ __launch_bounds__(kThreads) void pool_grow_kernel(GrowArgs p) {
+  __shared__ int lds[kThreads / 64];
+  __shared__ int cu[kSmallBatch + 1], old[kSmallBatch], base[kSmallBatch];
+  __shared__ uint8_t copies[kSmallBatch];
+  __shared__ int slot_page[kSlots], growers[kSlots], lowest[kSlots];
+  __shared__ int list[kSmallWanted];
+  const int tid = threadIdx.x, mask = (1 << p.page_shift) - 1;
+  for (int b = tid; b <= p.batch; b += kThreads) cu[b] = p.cu[b];
+  for (int i = tid; i < kSlots; i += kThreads) {
+    slot_page[i] = -1;
+    growers[i] = 0;
+    lowest[i] = INT_MAX;
+  }
+  // free pages: a thread's are next to each other, in eights
+  const int per = (int)((p.pages + kThreads - 1) / kThreads + 7) / 8;   // at most 8
+  uint64_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t page0 = ((int64_t)tid * per + i) * 8;
+    if (i < per && page0 < p.pages) bits |= (uint64_t)free_bits(p, page0) << (8 * i);
+  }
+  Want w{};
+  w.shared = -1;
+  if (tid < p.batch) w = want_of(p, tid);
+  const int holders = w.shared >= 0 ? p.refs[w.shared] : 0;
+  __syncthreads();
+  // sequences that grow on one shared page meet in its place; there are twice as many places as sequences
+  int at = 0;
+  if (w.shared >= 0) {
+    at = (int)((uint32_t)w.shared * 2654435761u >> 21) & (kSlots - 1);
+    for (;;) {
+      const int was = atomicCAS(&slot_page[at], -1, w.shared);
+      if (was == -1 || was == w.shared) break;
+      at = (at + 1) & (kSlots - 1);
+    }
+    atomicAdd(&growers[at], 1);
+    atomicMin(&lowest[at], tid);
+  }
+  __syncthreads();
+  const bool copy = w.shared >= 0 && !(growers[at] == holders && lowest[at] == tid);
+  int wanted, found;
+  const int mine = block_scan(tid < p.batch ? w.past - w.first + copy : 0, wanted, lds);
+  int rank = block_scan(__popcll(bits), found, lds);
+  const int64_t page0 = (int64_t)tid * per * 8;
+  // (offsets that fall may want more than the host has counted, and get no more than this)
+  found = min(found, kSmallWanted);
+  while (bits && rank < min(wanted, kSmallWanted)) {
+    list[rank++] = (int)page0 + __builtin_ctzll(bits);
+    bits &= bits - 1;
+  }
+  if (tid < p.batch) {
+    old[tid] = w.len;
+    base[tid] = mine;
+    copies[tid] = copy;
+  }
+  __syncthreads();
+  auto fresh = [&](int i) { return i < found ? list[i] : -1; };
+  // slots and positions, before the entries they are read from change
+  for (int64_t t = tid; t < p.tokens; t += kThreads) {
+    int lo = 0, hi = p.batch;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid + 1] > t) hi = mid; else lo = mid + 1;
+    }
+    int64_t slot = -1;
+    int pos = 0;
+    const int start = lo < p.batch ? (int)min((int64_t)max(cu[lo], 0), p.tokens) : 0;
+    if (lo < p.batch && t >= start) {
+      const int64_t to = (int64_t)old[lo] + (t - start);
+      pos = (int)min(to, (int64_t)INT_MAX);
+      if (to < (int64_t)p.width << p.page_shift) {
+        const int c = (int)(to >> p.page_shift), first = (old[lo] + mask) >> p.page_shift;
+        int page;
+        if (c >= first) page = fresh(base[lo] + copies[lo] + c - first);
+        else if (copies[lo]) page = fresh(base[lo]);
+        else page = p.table[(int64_t)lo * p.width + c];
+        if (page >= 0 && page < p.pages) slot = ((int64_t)page << p.page_shift) + (to & mask);
+      }
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+  if (tid == 0) *p.missing = max(wanted - found, 0);
+  if (tid < p.batch) {
+    int32_t* row = p.table + (int64_t)tid * p.width;
+    int s = -1, d = -1;
+    if (copy && (d = fresh(mine)) >= 0) {
+      s = w.shared;
+      row[w.len >> p.page_shift] = d;
+      p.refs[d] = 1;
+      atomicSub(&p.refs[s], 1);
+    }
+    p.src[tid] = s;
+    p.dst[tid] = d;
+    p.lens[tid] = w.longer;
+  }
+  // new entries: found by the page they are the next of
+  for (int i = tid; i < wanted; i += kThreads) {
+    int lo = 0, hi = p.batch;              // the last sequence that wants its first page at i or before
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (base[mid] > i) hi = mid; else lo = mid + 1;
+    }
+    --lo;
+    const int c = i - base[lo] - copies[lo];
+    if (c < 0) continue;                   // the copy
+    const int page = fresh(i);
+    p.table[(int64_t)lo * p.width + ((old[lo] + mask) >> p.page_shift) + c] = page;
+    if (page >= 0) p.refs[page] = 1;
+  }
+}
+
 struct PoolArgs {
   int32_t* refs;
   int32_t* table;
@@ -347,6 +465,11 @@ hipError_t launch_pool_grow(const moe_page_pool& pool, int64_t tokens, const int
   a.free_in = take(chunks);
   a.old = take(pool.batch); a.base = take(pool.batch); a.copies = take(pool.batch);
   a.growers = take(pool.pages); a.lowest = take(pool.pages); a.list = take(pool.pages);
+  if (pool.batch <= kSmallBatch && pool.pages <= kSmallPages && tokens <= kSmallTokens &&
+      2 * (int64_t)pool.batch + tokens / pool.page_size <= kSmallWanted) {
+    hipLaunchKernelGGL(pool_grow_kernel, dim3(1), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(pool_plan_kernel, dim3((unsigned)chunks + 1), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -364,10 +487,13 @@ hipError_t launch_pool_fork(const moe_page_pool& pool, const int32_t* parents, h
   if (pool.batch == 0) return hipSuccess;
   const PoolArgs a = pool_args(pool);
   // columns a workgroup owns: one for large batches, whose entries are its threads' registers
-  const int cols = std::clamp(4 * kThreads / pool.batch, 1, 64);
+  // (256 sequences: 5.8 us with an entry a thread, 11.6 with four)
+  const int cols = std::clamp(kThreads / pool.batch, 1, 64);
   const unsigned groups = (unsigned)((pool.width + cols - 1) / cols) + 1;
   const int64_t most = (int64_t)pool.batch * cols;
-  if (most <= 4 * kThreads)
+  if (most <= kThreads)
+    hipLaunchKernelGGL((pool_fork_kernel<1>), dim3(groups), dim3(kThreads), 0, st, a, parents, cols);
+  else if (most <= 4 * kThreads)
     hipLaunchKernelGGL((pool_fork_kernel<4>), dim3(groups), dim3(kThreads), 0, st, a, parents, cols);
   else if (most <= 16 * kThreads)
     hipLaunchKernelGGL((pool_fork_kernel<16>), dim3(groups), dim3(kThreads), 0, st, a, parents, cols);
