@@ -115,6 +115,17 @@ __device__ __forceinline__ uint32_t bit_of(uint64_t x, int i) {
   const uint32_t w = i < 32 ? (uint32_t)x : (uint32_t)(x >> 32);
   return i < 64 ? w >> (i & 31) & 1 : 0;
 }
+// f over all lanes, in all of them; `none` is f's neutral value.
+template <class F>
+__device__ __forceinline__ int wave_all(int x, int none, F f) {
+  x = f(x, __builtin_amdgcn_update_dpp(none, x, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+  x = f(x, __builtin_amdgcn_update_dpp(none, x, 0x112, 0xF, 0xF, false));
+  x = f(x, __builtin_amdgcn_update_dpp(none, x, 0x114, 0xF, 0xF, false));
+  x = f(x, __builtin_amdgcn_update_dpp(none, x, 0x118, 0xF, 0xF, false));
+  x = f(x, __builtin_amdgcn_update_dpp(none, x, 0x142, 0xA, 0xF, false));   // lane 15 of a row to the next
+  x = f(x, __builtin_amdgcn_update_dpp(none, x, 0x143, 0xC, 0xF, false));   // lane 31 to rows 2 and 3
+  return __builtin_amdgcn_readlane(x, 63);
+}
 __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int b, int tok,
                                         bool row_live) {
   const int lane = threadIdx.x & 63;       // a new token per lane
@@ -132,18 +143,17 @@ __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int
     if (p.window > 0) m &= ~low_bits(lane + 1 - p.window) | low_bits(p.sinks - r.ctx);
   }
   m &= low_bits(r.len - r.ctx) & ~low_bits(-r.ctx);
+  auto either = [](int a, int b) { return a | b; };
+  const int any_lo = wave_all((int)(uint32_t)m, 0, either);
+  const int any_hi = wave_all((int)(uint32_t)(m >> 32), 0, either);
   Seen s;
-  uint32_t any0 = (uint32_t)m, any1 = (uint32_t)(m >> 32);
-  int first = live ? pos : INT_MAX, last = live ? pos : -1;
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) {
-    any0 |= __shfl_xor(any0, i);
-    any1 |= __shfl_xor(any1, i);
-    first = min(first, __shfl_xor(first, i));
-    last = max(last, __shfl_xor(last, i));
+  s.any = (uint64_t)(uint32_t)any_hi << 32 | (uint32_t)any_lo;
+  int first = INT_MAX, last = -1;          // rows' positions, which a window goes by
+  const bool some = __ballot(live) != 0;
+  if (p.window > 0) {
+    first = wave_all(live ? pos : INT_MAX, INT_MAX, [](int a, int b) { return min(a, b); });
+    last = wave_all(live ? pos : -1, -1, [](int a, int b) { return max(a, b); });
   }
-  s.any = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(any1) << 32 |
-          (uint32_t)__builtin_amdgcn_readfirstlane(any0);
   const int at = __shfl(pos, tok);
   const int there = __shfl((int)live, tok);   // by all lanes: any may be asked
   s.keeps = row_live && there;
@@ -152,7 +162,6 @@ __device__ __forceinline__ Seen seen_of(const DecodeArgs& p, const Range& r, int
   auto start = [&](int q) { return p.window > 0 ? max(q + 1 - p.window, 0) : 0; };
   s.row_lo = s.keeps ? start(at) : INT_MAX;
   s.row_sinks = s.keeps ? sinks : 0;
-  const bool some = first != INT_MAX;
   s.lo = __builtin_amdgcn_readfirstlane(some ? start(first) : INT_MAX);
   s.sinks = __builtin_amdgcn_readfirstlane(some ? sinks : 0);
   s.all_lo = __builtin_amdgcn_readfirstlane(some ? start(last) : INT_MAX);
@@ -395,7 +404,7 @@ __device__ __forceinline__ void finish(const DecodeArgs& p, const Part& pc, int 
   }
 }
 
-// Up to 16 rows for a key-value head: each of 4 waves takes every fourth step of 32 keys,
+// Up to 16 rows for a key-value head (TREE: in each of its row groups): each of 4 waves takes every fourth step of 32 keys,
 // from memory to registers.
 template <int D, bool FP8, bool TREE>
 __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
@@ -413,9 +422,10 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
   const int kp = wave;
 
   const uint32_t wg = p.first + blockIdx.x;
-  const int piece = wg / p.hkv;
-  const int h = wg - piece * p.hkv;
-  constexpr int rg = 0;
+  const int per_piece = TREE ? p.hkv * p.rgroups : p.hkv;
+  const int piece = wg / per_piece;
+  const int rest = wg - piece * per_piece;
+  const int rg = TREE ? rest / p.hkv : 0, h = rest - rg * p.hkv;
   Piece pc;
   if (!find_piece<true, TREE>(p, piece, pc)) return;
   while (pc.at < pc.end) {
@@ -424,18 +434,13 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
   const int len = pt.rng.len, lo = pt.rng.lo, first = pt.first, last = pt.last;
 
   // this lane's row: token, head and the keys it keeps [row_lo, row_hi)
-  const int row = col;
+  const int row = TREE ? rg * 16 + col : col;
   const bool row_live = row < p.rows;
   const int tok = row_live ? row / p.group : 0;
   const int head = row_live ? h * p.group + row - tok * p.group : 0;
   const int64_t qrow = (int64_t)pt.b * p.q_len + tok;
   const int row_hi = len - p.q_len + 1 + tok;
   const int row_lo = p.window > 0 ? row_hi - p.window : 0;
-  // every row keeps the keys of [all_lo, all_hi)
-  Seen seen;
-  if constexpr (TREE) seen = seen_of(p, pt.rng, pt.b, tok, row_live);
-  const int all_hi = TREE ? pt.rng.ctx : len - p.q_len + 1;
-  const int all_lo = TREE ? seen.all_lo : p.window > 0 ? len - p.window : 0;
 
   bf16x8 qf[NF];
 #pragma unroll
@@ -455,6 +460,10 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs p) {
   float m = kNoMax, l = 0.f;
 
   Pages<TREE> pages(p, pt);
+  Seen seen;                                  // after the loads of q and pages have gone out
+  if constexpr (TREE) seen = seen_of(p, pt.rng, pt.b, tok, row_live);
+  const int all_hi = TREE ? pt.rng.ctx : len - p.q_len + 1;   // every row keeps [all_lo, all_hi)
+  const int all_lo = TREE ? seen.all_lo : p.window > 0 ? len - p.window : 0;
   const char* kh = p.k + h * p.sh;
   const char* vh = p.v + h * p.sh;
   const int page_mask = (1 << p.page_shift) - 1;
@@ -721,10 +730,6 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
   const int64_t qrow = (int64_t)pt.b * p.q_len + tok;
   const int row_hi = len - p.q_len + 1 + tok;
   const int row_lo = p.window > 0 ? row_hi - p.window : 0;
-  Seen seen;
-  if constexpr (TREE) seen = seen_of(p, pt.rng, pt.b, tok, row_live);
-  const int all_hi = TREE ? pt.rng.ctx : len - p.q_len + 1;
-  const int all_lo = TREE ? seen.all_lo : p.window > 0 ? len - p.window : 0;
 
   bf16x8 qf[NF];
 #pragma unroll
@@ -740,6 +745,10 @@ __global__ __launch_bounds__(64 * RT * KP, (ONE || D < 512) ? 2 : 1) void attn_d
   float m = kNoMax, l = 0.f;
 
   Pages<TREE> pages(p, pt);
+  Seen seen;                                  // after the loads of q and pages have gone out
+  if constexpr (TREE) seen = seen_of(p, pt.rng, pt.b, tok, row_live);
+  const int all_hi = TREE ? pt.rng.ctx : len - p.q_len + 1;   // every row keeps [all_lo, all_hi)
+  const int all_lo = TREE ? seen.all_lo : p.window > 0 ? len - p.window : 0;
   const int page_mask = (1 << p.page_shift) - 1;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   // a wave stages rows wave * WR .. of a step, in one 16-key tile and so one page
@@ -1064,6 +1073,15 @@ int64_t longest_walk(const moe_attn_config& c, const DecodeArgs& a) {
   return std::min(longest, (int64_t)c.window + a.sinks + c.q_len + 64);
 }
 
+// Row groups of 16 for the kernel without LDS where there are more rows, but so few keys and
+// workgroups that it is one launch which ends sooner than the others, though every group reads
+// the keys again; 0: the others.  8 nodes of 32 heads on 8 of 128, 300 keys: 12.3 us
+int narrow_groups(const moe_attn_config& c, int64_t bytes) {
+  const int64_t rows = (int64_t)c.q_len * (c.heads_q / c.heads_kv), groups = (rows + 15) / 16;
+  const int64_t workgroups = c.batch * c.heads_kv * groups;
+  return c.head_dim < 512 && rows > 16 && workgroups <= 512 && whole_sequences(bytes, 0, false) ? (int)groups : 0;
+}
+
 hipError_t launch_join(const moe_attn_config& c, DecodeArgs a, hipStream_t st) {
 #define MOE_JOIN(D) \
   case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), grid, dim3(256), 0, st, a); break;
@@ -1087,20 +1105,21 @@ hipError_t launch_decode(const moe_attn_config& c, const moe_rows& q, const moe_
   a.rows = d.rows; a.rgroups = d.rgroups;
   const int eb = kv.format == MOE_KV_FP8 ? 1 : 2;
   const bool one = kv.k == kv.v && (eb == 2 || kv.k_scale == kv.v_scale);
-  const bool whole = whole_sequences(
-      longest_walk<TREE>(c, a) * c.head_dim * eb * (one ? 1 : 2),
-      (int64_t)c.batch * c.heads_kv * d.rgroups, row_tiles(d.rows, c.head_dim) > 1);
+  const int64_t bytes = longest_walk<TREE>(c, a) * c.head_dim * eb * (one ? 1 : 2);
+  const int narrow = TREE ? narrow_groups(c, bytes) : 0;
+  if (narrow) a.rgroups = narrow;
+  const int rt = narrow ? 1 : row_tiles(d.rows, c.head_dim);
+  const bool whole = narrow || whole_sequences(bytes, (int64_t)c.batch * c.heads_kv * d.rgroups, rt > 1);
   a.pieces = whole ? 0 : d.pieces;
-  a.tile_shift = row_tiles(d.rows, c.head_dim) == 1 ? 7 : 6;
+  a.tile_shift = rt == 1 ? 7 : 6;
   const size_t rows = (size_t)d.slots * c.heads_kv * d.rows;
   char* w = static_cast<char*>(ws);
   a.part_o = reinterpret_cast<float*>(w); w += up256(rows * c.head_dim * 4);
   a.part_m = reinterpret_cast<float*>(w); w += up256(rows * 4);
   a.part_l = reinterpret_cast<float*>(w); w += up256(rows * 4);
-  a.meta = reinterpret_cast<int2*>(w);
-  const int64_t cut = row_tiles(d.rows, c.head_dim) == 1 ? d.pieces : d.slots;
-  const int64_t workgroups = (whole ? c.batch : cut) * c.heads_kv * d.rgroups;
-  const int rt = row_tiles(d.rows, c.head_dim);
+  a.meta = reinterpret_cast<int2*>(narrow ? ws : w);
+  const int64_t cut = rt == 1 ? d.pieces : d.slots;
+  const int64_t workgroups = (whole ? c.batch : cut) * c.heads_kv * a.rgroups;
   const bool f8 = kv.format == MOE_KV_FP8;
 #define MOE_ROWS(D, F, R, KP, O)                                                              \
   hipLaunchKernelGGL((attn_decode_rows_kernel<D, F, R, KP, O, TREE>), grid, dim3(64 * R * KP), 0, st, a)

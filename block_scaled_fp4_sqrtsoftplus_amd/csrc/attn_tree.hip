@@ -20,7 +20,11 @@ hipError_t launch_attn_tree(const moe_attn_config& c, int sinks, const moe_rows&
                             const int32_t* lens, const uint64_t* masks, const moe_rows& out,
                             float* lse, void* ws, hipStream_t st) {
   if (c.batch == 0) return hipSuccess;
-  if (masks && tree_rows_apply(c))
+  const int64_t tables = (int64_t)table_width * kv.page_size;
+  const int64_t longest = c.window > 0 ? std::min(tables, (int64_t)c.window + sinks + c.q_len + 64) : tables;
+  const bool f8 = kv.format == MOE_KV_FP8, one = kv.k == kv.v && (!f8 || kv.k_scale == kv.v_scale);
+  const bool narrow = narrow_groups(c, longest * c.head_dim * (f8 ? 1 : 2) * (one ? 1 : 2)) > 0;
+  if (masks && tree_rows_apply(c) && !narrow)
     return launch_tree_rows(c, sinks, q, kv, table, table_width, lens, masks, out, lse, ws, st);
   return launch_decode<true>(c, q, kv, table, table_width, lens, masks, sinks, out, lse, ws, st);
 }
