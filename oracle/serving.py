@@ -51,20 +51,17 @@ def attend(q, k, v, keep, scale):
     group = heads // k.shape[0]
     out, absv = np.zeros(q.shape), np.zeros(q.shape)
     lse, size = np.full((rows, heads), -np.inf), np.zeros((rows, heads))
-    for i in range(rows):
-        at = np.flatnonzero(keep[i])
-        if not len(at):
-            continue
-        for h in range(heads):
-            kh, vh = k[h // group][at], v[h // group][at]
-            s = scale * (kh @ q[i, h])
-            m = s.max()
-            e = np.exp(s - m)
-            t = e.sum()
-            lse[i, h] = m + np.log(t)
-            out[i, h] = (e / t) @ vh
-            absv[i, h] = (e / t) @ np.abs(vh)
-            size[i, h] = (abs(scale) * (np.abs(kh) @ np.abs(q[i, h]))).max()
+    some = keep.any(1)
+    for h in range(heads):
+        kh, vh = k[h // group], v[h // group]
+        s = np.where(keep, scale * (q[:, h] @ kh.T), -np.inf)
+        m = np.where(some, s.max(1, initial=-np.inf), 0.0)
+        e = np.exp(s - m[:, None])
+        t = np.where(some, e.sum(1), 1.0)
+        p = e / t[:, None]
+        lse[some, h] = (m + np.log(t))[some]
+        out[:, h], absv[:, h] = p @ vh, p @ np.abs(vh)
+        size[:, h] = np.where(keep, abs(scale) * (np.abs(q[:, h]) @ np.abs(kh).T), 0.0).max(1, initial=0.0)
     return out, lse, absv, size
 
 

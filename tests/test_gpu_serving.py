@@ -188,6 +188,82 @@ def test_attn_tree_values_out_of_range(hq, hkv, dim, fp8):
     assert (out == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("batch,hq,hkv,dim,nodes,most,fp8", [
+    (70, 16, 1, 128, 5, 700, False),       # more sequences than lanes of a wave, cut; 80 rows
+    (100, 16, 8, 64, 35, 150, False),      # fewer pieces than sequences, 70 rows
+    (100, 12, 4, 64, 61, 150, True),
+    (260, 16, 8, 64, 33, 60, False),       # whole sequences: none is cut
+    (40, 20, 2, 256, 20, 90, True),        # 200 rows: eight waves of 32
+    (9, 64, 1, 512, 4, 300, True),         # 256 rows of 512 elements
+])
+def test_attn_tree_of_many_sequences(batch, hq, hkv, dim, nodes, most, fp8):
+    rng = np.random.default_rng(batch + nodes)
+    contexts = [int(x) for x in rng.integers(0, most + 1, batch)]
+    contexts[3] = most
+    p = _Paged(rng, [c + nodes for c in contexts], hkv, dim, 16, fp8)
+    parents = _parents(rng, batch, nodes, 0.1)
+    parents[5] = -2
+    masks = serving.tree_masks(parents.tolist())[0]
+    q = _vals(rng, batch * nodes, hq, dim)
+    a = moe.TreeAttention(p.cache, batch, hq, nodes)
+    a.ws.fill_(0xFF)
+    args = dev_bf16(q), dev(p.table), dev(np.array(contexts, np.int32)), dev(_bits(masks))
+    out, lse = a(*args, want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, _tree_reference(p, q, contexts, masks, dim ** -0.5), dim)
+    assert torch.equal(a(*args), out)
+
+
+@pytest.mark.parametrize("hq,hkv,dim,nodes", [(4, 2, 128, 6), (8, 1, 128, 12), (8, 1, 64, 40), (6, 1, 512, 20)])
+def test_attn_tree_peaked_and_negative_scale(hq, hkv, dim, nodes):
+    # scores far apart: the running maximum rises late and by a lot
+    rng = np.random.default_rng(dim + nodes)
+    contexts = [400, 33]
+    p = _Paged(rng, [c + nodes for c in contexts], hkv, dim, 32, kv_scale=4.0)
+    q = _vals(rng, 2 * nodes, hq, dim, scale=4.0)
+    masks = serving.tree_masks(_parents(rng, 2, nodes).tolist())[0]
+    for scale in (1.0, -1.0):
+        out, lse = moe.attn_tree(dev_bf16(q), p.cache, dev(p.table), dev(np.array(contexts, np.int32)),
+                                 dev(_bits(masks)), scale=scale, want_lse=True)
+        torch.cuda.synchronize()
+        _check(out, lse, _tree_reference(p, q, contexts, masks, scale), dim)
+
+
+@pytest.mark.parametrize("fp8,hq", [(False, 2), (True, 2), (False, 40), (True, 40)])
+def test_far_pages_of_a_large_cache(fp8, hq):
+    # 4.9 GiB (bf16) or 2.4 GiB (FP8, past 2^31 bytes): drafted rows copied, moved and attended in the last pages
+    rng = np.random.default_rng(50 + hq)
+    hkv, page, n, nodes, dim = 2, 64, 150, 12, 128
+    pages = int((5.2e9 if not fp8 else 2.6e9) / (hkv * page * dim * (1 if fp8 else 2)))
+    cache = moe.KVCache.empty(pages, page, hkv, dim, moe.KV_FP8 if fp8 else moe.KV_BF16, shared=True)
+    table = np.array([[pages - 1, 7, pages - 2]], np.int32)
+    at = np.arange(n + nodes)
+    slots = table[0, at // page].astype(np.int64) * page + at % page
+    k, q = _vals(rng, n + nodes, hkv, dim), _vals(rng, nodes, hq, dim)
+    moe.kv_append(cache, dev_bf16(k), None, dev(slots))
+    moe.kv_copy_pages(cache, dev(np.array([7], np.int32)), dev(np.array([pages - 5], np.int32)))
+    table[0, 1] = pages - 5
+    parents = _parents(rng, 1, nodes, 0.0)
+    masks = serving.tree_masks(parents.tolist())[0]
+    ctx = dev(np.array([n], np.int32))
+    out, lse = moe.attn_tree(dev_bf16(q), cache, dev(table), ctx, dev(_bits(masks)), want_lse=True)
+    torch.cuda.synchronize()
+    rows = _f(k)
+    if fp8:
+        from test_gpu_attention import _quant_rows
+        rows = attention.fp8_values(*_quant_rows(rows))
+    rows = rows.swapaxes(0, 1)
+    _check(out, lse, serving.attend(_f(q), rows, rows, serving.tree_keep(masks[0], n, nodes), dim ** -0.5), dim)
+    path = dev(np.array([[2, 5, 11] + [0] * (nodes - 3)], np.int32))
+    moe.kv_compact(cache, dev(table), ctx, path, dev(np.array([3], np.int32)))
+    kept = np.concatenate([rows[:, :n], rows[:, [n + 2, n + 5, n + 11]]], 1)
+    out, lse = moe.attn_decode(dev_bf16(q[:1]), cache, dev(table), dev(np.array([n + 3], np.int32)), want_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, attention.attend(_f(q[:1]), kept, kept, n + 2, dim ** -0.5), dim)
+    del cache
+    torch.cuda.empty_cache()
+
+
 def test_attn_tree_of_a_chain_is_decode():
     # the same keys, rows and order of sums
     rng = np.random.default_rng(3)
@@ -449,13 +525,14 @@ def _as_pool(o):
 
 @pytest.mark.parametrize("pages,page,batch,width,seed", [
     (40, 16, 5, 7, 0), (40, 16, 5, 7, 1), (12, 32, 4, 5, 2), (300, 64, 70, 3, 3), (20000, 16, 9, 40, 4), (1, 16, 2, 2, 5),
-    (2500, 16, 1100, 2, 6), (9, 4096, 3, 3, 7)])
+    (2500, 16, 1100, 2, 6), (9, 4096, 3, 3, 7),
+    (70000, 16, 9, 40, 8), (900, 16, 40, 3000, 9)])
 def test_pool_follows_the_oracle(pages, page, batch, width, seed):
     rng = random.Random(seed)
     pool, want = moe.PagePool.empty(pages, page, batch, width), serving.Pool(pages, page, batch, width)
     pool.ws.fill_(0xFF)
-    if pages == 20000:                      # the first pages are taken, but some: free ones in several chunks
-        want.refs = [0 if i % 8191 == 5 or i > 19990 else 1 for i in range(pages)]
+    if pages in (20000, 70000):             # the first pages are taken, but some: free ones in several chunks
+        want.refs = [0 if i % 8191 == 5 or i > pages - 10 else 1 for i in range(pages)]
         pool.refs.copy_(torch.tensor(want.refs, dtype=torch.int32))
     short = 0
     for _ in range(25):
@@ -630,6 +707,26 @@ def test_a_captured_step_replays():
             assert torch.equal(a, b)
         moe.attn_decode(q[:batch], cache, pool.table, pool.lens)      # eager work between
         torch.cuda.synchronize()
+
+
+def test_two_calls_at_once():
+    # objects of their own on two streams, over one cache
+    rng = np.random.default_rng(41)
+    p = _Paged(rng, [3000, 900, 2000], 2, 128, 16)
+    table, ctx = dev(p.table), dev(p.lens - 20)
+    qs = [dev_bf16(_vals(rng, 60, 16, 128)) for _ in range(2)]
+    masks, _ = moe.tree_masks(dev(_parents(rng, 3, 20, 0.0)))
+    want = [moe.attn_tree(q, p.cache, table, ctx, masks) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = [moe.TreeAttention(p.cache, 3, 16, 20) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, a, q in zip(streams, calls, qs):
+            with torch.cuda.stream(s):
+                got.append(a(q, table, ctx, masks))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_on_another_stream():
