@@ -728,15 +728,22 @@ namespace {
 
 // The work of all sequences, end to end, is cut into equal pieces, so that one
 // round of workgroups takes them.  With four rounds of whole sequences nothing is
-// cut: workgroups that end early take the next ones.
+// cut: workgroups that end early take the next ones (288 sequences of 200 to 2048 keys
+// on 8 heads of 128: 317 us, cut 322).
+//
+// Eight groups of 32 rows in a workgroup read keys once where four would read them twice and
+// turn FP8 into bf16 twice: 64 nodes of 12 sequences of 3000 to 6000, 4 heads on each of 8, 128 elements
+// 85 us (bf16 90) and 95 with four (95), 64 elements 61 (62) and 67 (63).  Up to 128 rows four hold
+// them all, but with 256 elements in FP8 a thread of four groups holds twice the codes of one
+// of eight and spills them: 32 nodes of 16 sequences 182 us with eight groups, 337 with four (bf16 182 and 157).
 struct TreePlan {
   int rows, rg, rgroups, pieces;   // rg: groups of 32 rows in a workgroup
   int64_t slots;
 };
-TreePlan tree_plan(const moe_attn_config& c) {
+TreePlan tree_plan(const moe_attn_config& c, bool f8) {
   TreePlan t;
   t.rows = c.q_len * (c.heads_q / c.heads_kv);
-  t.rg = c.head_dim < 512 && t.rows > 128 ? 8 : 4;
+  t.rg = c.head_dim < 512 && (t.rows > 128 || (c.head_dim == 256 && f8)) ? 8 : 4;
   t.rgroups = (t.rows + 32 * t.rg - 1) / (32 * t.rg);
   const int64_t per = (int64_t)c.heads_kv * t.rgroups;
   // workgroups that the GPU holds at once: two on a CU, of eight waves one
@@ -749,8 +756,11 @@ TreePlan tree_plan(const moe_attn_config& c) {
 }  // namespace
 
 size_t tree_rows_ws_bytes(const moe_attn_config& c) {
-  const TreePlan t = tree_plan(c);
-  const size_t rows = t.pieces ? (size_t)t.slots * c.heads_kv * t.rgroups * t.rg * 32 : 0;
+  size_t rows = 0;                 // of the caches' types the one that takes more
+  for (bool f8 : {false, true}) {
+    const TreePlan t = tree_plan(c, f8);
+    if (t.pieces) rows = std::max(rows, (size_t)t.slots * c.heads_kv * t.rgroups * t.rg * 32);
+  }
   return up256(rows * c.head_dim * 4) + 2 * up256(rows * 4) + up256((size_t)c.batch * 8) + 256;
 }
 
@@ -758,7 +768,9 @@ hipError_t launch_tree_rows(const moe_attn_config& c, int sinks, const moe_rows&
                             const moe_kv_cache& kv, const int32_t* table, int table_width,
                             const int32_t* lens, const uint64_t* masks, const moe_rows& out,
                             float* lse, void* ws, hipStream_t st) {
-  const TreePlan t = tree_plan(c);
+  const bool one = kv.k == kv.v && (kv.format != MOE_KV_FP8 || kv.k_scale == kv.v_scale);
+  const bool f8 = kv.format == MOE_KV_FP8;
+  const TreePlan t = tree_plan(c, f8);
   DecodeArgs a = decode_args(c, q, kv, table, table_width, lens, out, lse);
   a.masks = masks; a.sinks = sinks;
   a.rows = t.rows; a.rgroups = t.rgroups; a.row_groups = t.rg;
@@ -766,8 +778,6 @@ hipError_t launch_tree_rows(const moe_attn_config& c, int sinks, const moe_rows&
   a.scale2 = (c.scale < 0.f ? -c.scale : c.scale) * kLog2e;
   a.tile_shift = 6;
   char* w = static_cast<char*>(ws);
-  const bool one = kv.k == kv.v && (kv.format != MOE_KV_FP8 || kv.k_scale == kv.v_scale);
-  const bool f8 = kv.format == MOE_KV_FP8;
   const bool cut = t.pieces > 0 &&
                    !whole_sequences(longest_walk<true>(c, a) * c.head_dim * (f8 ? 1 : 2) * (one ? 1 : 2),
                                     (int64_t)c.batch * c.heads_kv * t.rgroups, true);
@@ -785,8 +795,10 @@ hipError_t launch_tree_rows(const moe_attn_config& c, int sinks, const moe_rows&
   hipLaunchKernelGGL((attn_tree_rows_kernel<D, F, O, G>), grid, dim3(64 * G * (D == 512 ? 2 : 1)), 0, st, a)
 #define MOE_TREE(D)                                                                            \
   case D:                                                                                      \
-    if (f8) { if (t.rg == 8) MOE_TREE_ROWS(D, true, false, 8); else MOE_TREE_ROWS(D, true, false, 4); }   \
-    else { if (t.rg == 8) MOE_TREE_ROWS(D, false, false, 8); else MOE_TREE_ROWS(D, false, false, 4); }    \
+    if (f8) { if (t.rg == 8) MOE_TREE_ROWS(D, true, false, 8);                                 \
+      else MOE_TREE_ROWS(D, true, false, D == 256 ? 8 : 4); }                                  \
+    else { if (t.rg == 8) MOE_TREE_ROWS(D, false, false, 8);                                   \
+      else MOE_TREE_ROWS(D, false, false, 4); }                                                \
     break;
   const hipError_t e = launch_workgroups((total + 7) / 8 * 8, [&](uint32_t first, dim3 grid) {
     a.first = first;

@@ -133,6 +133,8 @@ def test_attn_tree(hq, hkv, dim, page, nodes, window, sinks, fp8, shared, by_tok
     (8, 2, 128, 2, True, [9001, 3, 0, 130]),
     (8, 2, 128, 9, False, [3000, 40, 0, 1111]),
     (4, 1, 128, 50, True, [2500, 64, 3]),
+    (8, 2, 256, 20, True, [2100, 0, 900, 15]),          # 80 rows of 256 elements
+    (8, 2, 256, 20, False, [2100, 0, 900, 15]),
     (12, 1, 512, 8, False, [1500, 700]),
     (2, 2, 64, 5, False, [60] * 130),                   # more sequences than lanes of a wave
 ])
