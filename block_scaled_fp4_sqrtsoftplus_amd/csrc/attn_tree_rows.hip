@@ -579,17 +579,27 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
       const int kb_next = kb + 1 == KB ? 0 : kb + 1;
       const int vb_next = ONE ? kb : vb ^ 1;
       const bool more = it + 1 < steps;
-      if constexpr (!ONE) fetch(1, vb_next, at0, pl, 0);
-      if (more) {
-        pl.find(tiles, at0 + BN, sub);
-        fetch(0, kb_next, at0 + BN, pl, 0);
-      }
+      auto load = [&]() __attribute__((always_inline)) {
+        if constexpr (!ONE) fetch(1, vb_next, at0, pl, 0);
+        if (more) {
+          pl.find(tiles, at0 + BN, sub);
+          fetch(0, kb_next, at0 + BN, pl, 0);
+        }
+      };
+      auto store = [&]() __attribute__((always_inline)) {
+        if (more) put(0, kb_next, 0);
+        if constexpr (!ONE) put(1, vb_next, 0);
+      };
+      // FP8 codes are on their way beside the weights alone: a register that the products had to
+      // take back from memory would wait for them
+      if constexpr (!FP8 || LATE) load();
       if constexpr (!LATE) products(begins);
       else if constexpr (!decltype(begins)::value) weights(at0 - BN, ok_before);
+      if constexpr (LATE) store();
       lds_barrier();
+      if constexpr (FP8 && !LATE) load();
       if constexpr (LATE) products(begins); else weights(at0, ok);
-      if (more) put(0, kb_next, 0);
-      if constexpr (!ONE) put(1, vb_next, 0);
+      if constexpr (!LATE) store();
       kb = kb_next;
       vb = vb_next;
       ok_before = ok;
