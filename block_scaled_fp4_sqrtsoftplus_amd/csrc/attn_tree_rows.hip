@@ -12,6 +12,19 @@
 // reads all of K and V from LDS for half as many products: LDS then is the
 // bound.  Keys come through the block table 16 rows at a time, bf16 straight
 // into LDS, FP8 through registers, turned into bf16 once for all waves.
+//
+// Which calls: more than 64 rows to a key-value head.  32 sequences of 1000 to 4096
+// keys, 26 nodes, 32 heads of 128 on 8 take 94 us here and 149 in the kernel for few rows, 8 of
+// 6000 to 8192 keys and 64 nodes 86 and 224 (FP8 94 and 303), 4 of 2000 to 4096, 40 nodes of 64
+// elements 25 and 49, 16 of 2000 to 4096, 16 nodes of 32 heads on one 512-element head 112 and 142.
+//
+// Bound by memory up to about 100 rows (the keys once: 32 sequences, 26 nodes 6.3 TB/s
+// inside the loop), by the matrix units and what stands between their products
+// beyond: 64 nodes of 8 sequences, FP8 69 us (507 TFLOP/s), 16 nodes of 64 heads
+// on one 512-element head 168 us (466 TFLOP/s).  A part of a sequence costs a workgroup 9 us before its
+// first step (its place in the work, pages, masks, first tiles: each waits for
+// the one before) and 2 behind its last; the partial results, 100 MB in the last
+// case, are joined in 9 to 18 us.
 #include <type_traits>
 
 #include "attn_decode_kernels.h"
@@ -196,7 +209,9 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
   constexpr int NG = D < 128 ? 1 : D / 128;
   constexpr int NT = ONE ? 1 : 2;
   // tiles of K (and of V); steps that are asked for ahead of the one that is
-  // computed: bf16 into LDS, FP8 into registers
+  // computed: bf16 into LDS, as many as two workgroups on a CU have room for, FP8 into registers.
+  // (32 keys a step and five tiles take as long as 64 and two.  512-element heads two steps ahead
+  // spill 30 registers: 202 us instead of 168 at 16 nodes of 64 heads.)
   constexpr int KB = ONE ? 3 : FP8 || SPLIT == 2 ? 2 : 2 * (RG / 4) * (D == 64 ? 2 : 1);
   constexpr int DIST = SPLIT == 2 ? 1 : !FP8 ? KB - 1 : RG == 8 && D < 256 ? 2 : 1;
   constexpr int SETS = FP8 ? DIST : 1;
@@ -229,7 +244,8 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
   const int h = __builtin_amdgcn_readfirstlane(rest / p.rgroups);
   const int rg = __builtin_amdgcn_readfirstlane(rest - h * p.rgroups);
   Work work;
-  constexpr int START = D == 512 ? 2 : 5;    // 13 us where a tile takes 2.6, 11 where it takes 5
+  // 13 us where a tile takes 2.6, 11 where it takes 5; 3 and 8 tiles were slower by 1 to 3%
+  constexpr int START = D == 512 ? 2 : 5;
   if (!find_work<START>(p, w, work)) return;
 
   // this lane's row: whether it is one, its token and head
