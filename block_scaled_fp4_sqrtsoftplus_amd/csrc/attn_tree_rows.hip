@@ -267,9 +267,9 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
   // rows are in one 16-key tile of the walk.  Its place in the row is permuted
   // on the global side, since the load writes LDS in lane order.
   constexpr int WR = 64 / C;                  // rows of a wave's load
-  auto row_of = [&](int i) { return wv * WR + here() / C + RS * i; };
+  auto row_of = [&](int i) { return wv * WR + (int)((here() & 63u) / C) + RS * i; };
   auto chunk = [&](int t, int r) {
-    return (here() % C) ^ (t ? v_swz<D>(r) : k_swz<D>(r));
+    return (int)((here() & 63u) % C) ^ (t ? v_swz<D>(r) : k_swz<D>(r));
   };
 
   while (work.at < work.end) {
