@@ -16,12 +16,12 @@
 // Which calls: more than 64 rows to a key-value head.  32 sequences of 1000 to 4096
 // keys, 26 nodes, 32 heads of 128 on 8 take 94 us here and 149 in the kernel for few rows, 8 of
 // 6000 to 8192 keys and 64 nodes 86 and 224 (FP8 94 and 303), 4 of 2000 to 4096, 40 nodes of 64
-// elements 25 and 49, 16 of 2000 to 4096, 16 nodes of 32 heads on one 512-element head 100 and 142.
+// elements 25 and 49, 16 of 2000 to 4096, 16 nodes of 32 heads on one 512-element head 97 and 142.
 //
 // Bound by memory up to about 100 rows (the keys once: 32 sequences, 26 nodes 6.3 TB/s
 // inside the loop), by the matrix units and what stands between their products
-// beyond: 64 nodes of 8 sequences, FP8 69 us (507 TFLOP/s), 16 nodes of 64 heads
-// on one 512-element head 164 us (477 TFLOP/s).  A part of a sequence costs a workgroup 9 us before its
+// beyond: 64 nodes of 8 sequences, FP8 67 us (522 TFLOP/s), 16 nodes of 64 heads
+// on one 512-element head 149 us (525 TFLOP/s).  A part of a sequence costs a workgroup 9 us before its
 // first step (its place in the work, pages, masks, first tiles: each waits for
 // the one before) and 2 behind its last; the partial results, 100 MB in the last
 // case, are joined in 9 to 18 us.
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
   // tiles of K (and of V); steps that are asked for ahead of the one that is
   // computed: bf16 into LDS, as many as two workgroups on a CU have room for, FP8 into registers.
   // (32 keys a step and five tiles take as long as 64 and two.  512-element heads two steps ahead
-  // spill 30 registers: 202 us instead of 168 at 16 nodes of 64 heads.)
+  // spilled 30 registers: 202 us instead of 168 at 16 nodes of 64 heads.)
   constexpr int KB = ONE ? 3 : FP8 || SPLIT == 2 ? 2 : 2 * (RG / 4) * (D == 64 ? 2 : 1);
   constexpr int DIST = SPLIT == 2 ? 1 : !FP8 ? KB - 1 : RG == 8 && D < 256 ? 2 : 1;
   constexpr int SETS = FP8 ? DIST : 1;
@@ -769,7 +769,7 @@ namespace {
 // turn FP8 into bf16 twice: 64 nodes of 12 sequences of 3000 to 6000, 4 heads on each of 8, 128 elements
 // 85 us (bf16 90) and 95 with four (95), 64 elements 61 (62) and 67 (63).  Up to 128 rows four hold
 // them all, but with 256 elements in FP8 a thread of four groups holds twice the codes of one
-// of eight and spills them: 32 nodes of 16 sequences 179 us with eight groups, 337 with four (bf16 182 and 157).
+// of eight and spills them: 32 nodes of 16 sequences 174 us with eight groups, 337 with four (bf16 182 and 157).
 struct TreePlan {
   int rows, rg, rgroups, pieces;   // rg: groups of 32 rows in a workgroup
   int64_t slots;
