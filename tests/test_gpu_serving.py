@@ -591,6 +591,35 @@ def test_pool_offsets_out_of_range_stay_in_bounds():
     assert slots.tolist() == [-1] * 3 and none.missing.item() == 2 and none.lens.tolist() == [1, 2]
 
 
+def test_pool_calls_of_nothing():
+    none = moe.PagePool.empty(8, 16, 0, 4)
+    slots, _, src, _ = none.grow(dev(np.array([0], np.int32)), 2)      # tokens of no sequence
+    assert slots.tolist() == [-1, -1] and src.numel() == 0 and none.missing.item() == 0
+    none.fork(dev(np.zeros(0, np.int32)))
+    none.trim()
+    pool = moe.PagePool.empty(8, 16, 2, 4)
+    slots, _, _, _ = pool.grow(dev(np.array([0, 0, 0], np.int32)), 0)
+    assert slots.numel() == 0 and pool.lens.tolist() == [0, 0]
+    pool.grow(dev(np.array([0, 17, 20], np.int32)), 20)
+    before = _state(pool)
+    pool.fork(dev(np.array([0, 1], np.int32)))                          # each its own
+    pool.trim(pool.lens)                                                # to the length that it has
+    assert _state(pool) == before and pool.lens.tolist() == [17, 3]
+
+
+@pytest.mark.parametrize("hq,hkv,dim,nodes", [(8, 2, 64, 3), (16, 2, 128, 12), (24, 1, 256, 8), (16, 1, 512, 16)])
+@pytest.mark.parametrize("pages,width", [(0, 2), (2, 0)])
+def test_attn_tree_of_no_pages(hq, hkv, dim, nodes, pages, width):
+    for kv in (moe.KV_BF16, moe.KV_FP8):
+        cache = moe.KVCache.empty(pages, 16, hkv, dim, kv)
+        masks = torch.ones((2, nodes), dtype=torch.int64, device="cuda")
+        table = torch.zeros((2, width), dtype=torch.int32, device="cuda")
+        q = torch.ones((2 * nodes, hq, dim), dtype=torch.bfloat16, device="cuda")
+        out, lse = moe.attn_tree(q, cache, table, dev(np.array([0, 20], np.int32)), masks, want_lse=True)
+        torch.cuda.synchronize()
+        assert not out.any() and bool((lse == -float("inf")).all())
+
+
 # ----------------------------------------------------------------------------
 # Together
 # ----------------------------------------------------------------------------
