@@ -39,7 +39,7 @@ struct GrowArgs {
   int32_t* base;           // [batch] how many pages the sequences before want
   int32_t* copies;         // [batch] whether the partly filled page is copied
   int32_t* growers;        // [pages] how many sequences grow on a shared page
-  int32_t* lowest;         // [pages] the first of them
+  int32_t* keeper;         // [pages] the smallest keep_key of theirs
   int32_t* list;           // [pages] the free pages in order
 };
 
@@ -102,6 +102,14 @@ __device__ __forceinline__ Want want_of(const GrowArgs& p, int b) {
   return w;
 }
 
+// Where all holders of a page grow, the one with the smallest key keeps it: the one with the most
+// tokens on it, of equals the first.  What it writes there is behind the tokens of all others, so
+// that they lose nothing, also where there is no page left for their copies.
+__device__ __forceinline__ int keep_key(const GrowArgs& p, const Want& w, int b) {
+  const int mask = (1 << p.page_shift) - 1;
+  return (mask - (w.len & mask)) << 16 | b;      // 12 bits and 16
+}
+
 // Workgroup 0: how many pages each sequence wants, and whether it copies the page it grows on.
 // The others: how many pages of a chunk are free.
 __global__ __launch_bounds__(kThreads) void pool_plan_kernel(GrowArgs p) {
@@ -121,16 +129,16 @@ __global__ __launch_bounds__(kThreads) void pool_plan_kernel(GrowArgs p) {
     if (s < 0) continue;
     any = true;
     atomicExch(&p.growers[s], 0);
-    atomicExch(&p.lowest[s], INT_MAX);
+    atomicExch(&p.keeper[s], INT_MAX);
   }
   if (__syncthreads_or(any)) {
     __threadfence();
     __syncthreads();
     for (int b = tid; b < p.batch; b += kThreads) {
-      const int s = want_of(p, b).shared;
-      if (s < 0) continue;
-      atomicAdd(&p.growers[s], 1);
-      atomicMin(&p.lowest[s], b);
+      const Want w = want_of(p, b);
+      if (w.shared < 0) continue;
+      atomicAdd(&p.growers[w.shared], 1);
+      atomicMin(&p.keeper[w.shared], keep_key(p, w, b));
     }
     __threadfence();
     __syncthreads();
@@ -144,8 +152,8 @@ __global__ __launch_bounds__(kThreads) void pool_plan_kernel(GrowArgs p) {
     if (b < p.batch) {
       w = want_of(p, b);
       if (w.shared >= 0) {
-        const int n = atomicAdd(&p.growers[w.shared], 0), low = atomicAdd(&p.lowest[w.shared], 0);
-        copy = !(n == p.refs[w.shared] && low == b);
+        const int n = atomicAdd(&p.growers[w.shared], 0), key = atomicAdd(&p.keeper[w.shared], 0);
+        copy = !(n == p.refs[w.shared] && key == keep_key(p, w, b));
       }
       need = w.past - w.first + copy;
     }
@@ -253,14 +261,14 @@ __global__ __launch_bounds__(kThreads) void pool_grow_kernel(GrowArgs p) {
   __shared__ int lds[kThreads / 64];
   __shared__ int cu[kSmallBatch + 1], old[kSmallBatch], base[kSmallBatch];
   __shared__ uint8_t copies[kSmallBatch];
-  __shared__ int slot_page[kSlots], growers[kSlots], lowest[kSlots];
+  __shared__ int slot_page[kSlots], growers[kSlots], keeper[kSlots];
   __shared__ int list[kSmallWanted];
   const int tid = threadIdx.x, mask = (1 << p.page_shift) - 1;
   for (int b = tid; b <= p.batch; b += kThreads) cu[b] = p.cu[b];
   for (int i = tid; i < kSlots; i += kThreads) {
     slot_page[i] = -1;
     growers[i] = 0;
-    lowest[i] = INT_MAX;
+    keeper[i] = INT_MAX;
   }
   // free pages: a thread's are next to each other, in eights
   const int per = (int)((p.pages + kThreads - 1) / kThreads + 7) / 8;   // at most 8
@@ -285,10 +293,11 @@ __global__ __launch_bounds__(kThreads) void pool_grow_kernel(GrowArgs p) {
       at = (at + 1) & (kSlots - 1);
     }
     atomicAdd(&growers[at], 1);
-    atomicMin(&lowest[at], tid);
+    atomicMin(&keeper[at], keep_key(p, w, tid));
   }
   __syncthreads();
-  const bool copy = w.shared >= 0 && !(growers[at] == holders && lowest[at] == tid);
+  const bool copy =
+      w.shared >= 0 && !(growers[at] == holders && keeper[at] == keep_key(p, w, tid));
   int wanted, found;
   const int mine = block_scan(tid < p.batch ? w.past - w.first + copy : 0, wanted, lds);
   int rank = block_scan(__popcll(bits), found, lds);
@@ -465,7 +474,7 @@ hipError_t launch_pool_grow(const moe_page_pool& pool, int64_t tokens, const int
   a.totals = take(2);
   a.free_in = take(chunks);
   a.old = take(pool.batch); a.base = take(pool.batch); a.copies = take(pool.batch);
-  a.growers = take(pool.pages); a.lowest = take(pool.pages); a.list = take(pool.pages);
+  a.growers = take(pool.pages); a.keeper = take(pool.pages); a.list = take(pool.pages);
   if (pool.batch <= kSmallBatch && pool.pages <= kSmallPages && tokens <= kSmallTokens &&
       2 * (int64_t)pool.batch + tokens / pool.page_size <= kSmallWanted) {
     hipLaunchKernelGGL(pool_grow_kernel, dim3(1), dim3(kThreads), 0, st, a);

@@ -120,7 +120,8 @@ size_t moe_pool_workspace_size(const moe_page_pool* pool);
  * lowest-numbered free pages, sequence by sequence.  A sequence that grows on
  * a partly filled page held by others too gets a fresh page in its place,
  * before its others, and the pair (src, dst) to copy, in every layer's cache, before the new rows are
- * stored; where all holders of such a page grow, the first of them keeps it.
+ * stored; where all holders of such a page grow, the one with the most tokens on it keeps it (of
+ * equals the first), so that its new rows are behind every other holder's tokens.
  *   cu         [batch + 1] int32, not decreasing (entries are clamped to [0, tokens])
  *   slots      [tokens] int64 receives the new tokens' slots (moe_kv_append):
  *              -1 for one past the sequence's end, on a page that was not to be had,

@@ -77,7 +77,9 @@ class Pool:
             self.refs[page] -= 1
 
     def grow(self, counts):
-        """Returns slots, positions, (src, dst) of each sequence, and how many pages were missing."""
+        """Returns slots, positions, (src, dst) of each sequence, and how many pages were missing.  Where all holders of
+        a partly filled page grow, the one with the most tokens on it keeps it (of equals the first): what it writes
+        there is behind the others' tokens, whether their copies are to be had or not."""
         size, cap = self.page_size, self.width * self.page_size
         free = iter([p for p, n in enumerate(self.refs) if n == 0])
         longer = [min(n + c, cap) for n, c in zip(self.lens, counts)]
@@ -86,11 +88,12 @@ class Pool:
         growers = {}
         for b, page in enumerate(held):
             growers.setdefault(page, []).append(b)
+        keeper = {page: max(bs, key=lambda b: (self.lens[b] % size, -b)) for page, bs in growers.items()}
         slots, positions, pairs, missing = [], [], [], 0
         for b, (n, m) in enumerate(zip(self.lens, longer)):
             pair, lost = (-1, -1), False
             mine = growers[held[b]]
-            if 0 <= held[b] < len(refs) and refs[held[b]] > 1 and not (len(mine) == refs[held[b]] and mine[0] == b):
+            if 0 <= held[b] < len(refs) and refs[held[b]] > 1 and not (len(mine) == refs[held[b]] and keeper[held[b]] == b):
                 page = next(free, -1)
                 if page < 0:
                     missing, lost = missing + 1, True

@@ -844,3 +844,58 @@ def test_refusals():
             moe.PagePool(*args)
     with pytest.raises(moe.MoeError):
         moe.PagePool(lens, table, lens, 24)
+
+
+def _nearly_full(pages, batch, width, free):
+    """A pool and its oracle in which only the pages `free` are not taken."""
+    pool, want = moe.PagePool.empty(pages, 16, batch, width), serving.Pool(pages, 16, batch, width)
+    want.refs = [int(i not in free) for i in range(pages)]
+    pool.refs.copy_(torch.tensor(want.refs, dtype=torch.int32))
+    return pool, want
+
+
+@pytest.mark.parametrize("pages", [40, 70000])         # grown in one launch and in three
+@pytest.mark.parametrize("cut", [[18, 25], [25, 18], [25, 25], [17, 31]])
+@pytest.mark.parametrize("spare", [0, 1])
+def test_a_shared_page_stays_with_its_longest_holder(pages, cut, spare):
+    free = [5, pages - 3, pages - 2][:2 + spare]
+    pool, want = _nearly_full(pages, 2, 4, free)
+    for p, parents in ((pool, dev(np.array([0, 0], np.int32))), (want, [0, 0])):
+        p.grow(*((dev(_cu([31, 0])), 31) if p is pool else ([31, 0],)))
+        p.fork(parents)
+        p.trim(dev(np.array(cut, np.int32)) if p is pool else cut)
+    slots, _, src, dst = pool.grow(dev(_cu([1, 1])), 2)
+    s, _, pairs, missing = want.grow([1, 1])
+    assert slots.tolist() == s and list(zip(src.tolist(), dst.tolist())) == pairs
+    assert pool.missing.item() == missing == 1 - spare and _state(pool) == tuple(_as_pool(want))
+    keeps = 0 if cut[0] >= cut[1] else 1
+    assert s[keeps] == (pages - 3) * 16 + cut[keeps] - 16 and pairs[keeps] == (-1, -1)
+    assert s[1 - keeps] == ((pages - 2) * 16 + cut[1 - keeps] - 16 if spare else -1)
+
+
+@pytest.mark.parametrize("pages", [14, 70000])
+@pytest.mark.parametrize("seed", range(3))
+def test_pool_short_of_pages_follows_the_oracle(pages, seed):
+    rng = random.Random(pages + seed)
+    free = rng.sample(range(pages), 12)
+    pool, want = _nearly_full(pages, 5, 6, free)
+    short = 0
+    for _ in range(40):
+        act = rng.choice(["grow", "grow", "fork", "cut"])
+        if act == "grow":
+            counts = [rng.choice([1, 2, 5, 20])] * 5 if rng.random() < 0.7 else [rng.choice([0, 1, 20]) for _ in range(5)]
+            slots, _, src, dst = pool.grow(dev(_cu(counts)), sum(counts))
+            s, _, pairs, missing = want.grow(counts)
+            assert slots.tolist() == s and list(zip(src.tolist(), dst.tolist())) == pairs
+            assert pool.missing.item() == missing
+            short += missing
+        elif act == "fork":
+            parents = [rng.choice([b, rng.randint(-1, 4)]) for b in range(5)]
+            pool.fork(dev(np.array(parents, np.int32)))
+            want.fork(parents)
+        else:
+            lens = [max(0, n - rng.choice([0, 0, 1, 3, 7, 12, 40])) for n in want.lens]
+            pool.trim(dev(np.array(lens, np.int32)))
+            want.trim(lens)
+        assert _state(pool) == tuple(_as_pool(want))
+    assert short > 0

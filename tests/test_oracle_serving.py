@@ -98,3 +98,61 @@ def test_pool_counts_are_those_of_its_table(seed):
                 page = p.table[b][j // 16]
                 if token is not None and page >= 0:
                     assert rows[page * 16 + j % 16] == token
+
+
+def test_a_shared_page_stays_with_its_longest_holder():
+    p = serving.Pool(2, 16, 2, 4)
+    p.grow([25, 0])
+    p.fork([0, 0])
+    p.trim([18, 25])
+    # no page is left, and rows 2 to 8 of the shared one are positions 18 to 24 of sequence 1
+    slots, _, pairs, missing = p.grow([3, 3])
+    assert slots == [-1, -1, -1, 25, 26, 27] and pairs == [(-1, -1)] * 2 and missing == 1
+
+
+@pytest.mark.parametrize("pages", [10, 14])
+@pytest.mark.parametrize("seed", range(8))
+def test_pool_short_of_pages_keeps_what_sequences_hold(seed, pages):
+    """Forks cut to different lengths inside a page, then grown until pages run out: no slot that is given out is a
+    row that another sequence holds."""
+    rng = random.Random(100 * pages + seed)
+    p = serving.Pool(pages, 16, 5, 6)
+    rows, story, short = {}, [[] for _ in range(5)], 0
+    for turn in range(80):
+        act = rng.choice(["grow", "grow", "fork", "cut"])
+        if act == "grow":
+            counts = [rng.choice([1, 2, 5, 20])] * 5 if rng.random() < 0.7 else [rng.choice([0, 1, 20]) for _ in range(5)]
+            before, tables = list(p.lens), [list(r) for r in p.table]
+            slots, _, pairs, missing = p.grow(counts)
+            short += missing
+            for a, z in pairs:
+                for r in range(16):
+                    if a >= 0:
+                        rows[z * 16 + r] = rows.get(a * 16 + r)
+            at = 0
+            for b, c in enumerate(counts):
+                for i in range(c):
+                    if slots[at] >= 0:
+                        page, row = divmod(slots[at], 16)
+                        for o in range(5):              # the other sequences as they are after the call
+                            held = [col for col, x in enumerate(p.table[o]) if x == page and tables[o][col] == page]
+                            assert all(o == b or col * 16 + row >= before[o] for col in held)
+                        rows[slots[at]] = (turn, b, i)
+                    if before[b] + i < p.lens[b]:
+                        story[b].append((turn, b, i) if slots[at] >= 0 else None)
+                    at += 1
+        elif act == "fork":
+            parents = [rng.choice([b, rng.randint(-1, 4)]) for b in range(5)]
+            p.fork(parents)
+            story = [list(story[x]) if x >= 0 else [] for x in parents]
+        else:
+            lens = [max(0, n - rng.choice([0, 0, 1, 3, 7, 12, 40])) for n in p.lens]
+            p.trim(lens)
+            story = [s[:n] for s, n in zip(story, lens)]
+        for b, s in enumerate(story):
+            assert len(s) == p.lens[b]
+            for j, token in enumerate(s):
+                page = p.table[b][j // 16]
+                if token is not None and page >= 0:
+                    assert rows[page * 16 + j % 16] == token
+    assert short > 0
