@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void pool_fill_kernel(GrowArgs p, uint32_t seq
       }
       p.src[b] = s;
       p.dst[b] = d;
-      p.lens[b] = longer;
+      p.lens[b] = copy && d < 0 ? len : longer;   // without its copy it stays as it is
     }
     return;
   }
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void pool_grow_kernel(GrowArgs p) {
     }
     p.src[tid] = s;
     p.dst[tid] = d;
-    p.lens[tid] = w.longer;
+    p.lens[tid] = copy && d < 0 ? w.len : w.longer;   // without its copy it stays as it is
   }
   // new entries: found by the page they are the next of
   for (int i = tid; i < wanted; i += kThreads) {

@@ -8,12 +8,19 @@ One step of speculative decoding, for every sequence of a pool:
     before = pool.lens.clone()
     masks, depths = tree_masks(parents)
     slots, _, src, dst = pool.grow(cu, tokens)              # room for the drafted tokens
+    masks = masks * (slots >= 0).view_as(masks)             # a node without a place is an empty one
     kv_copy_pages(cache, src, dst)                          # ... in every layer's cache
     positions = (before[:, None] + depths).flatten()
     q = kv_append(cache, k, v, slots, positions, rope, q)
     out = attend(q, pool.table, before, masks)              # a TreeAttention
     kv_compact(cache, pool.table, before, path, counts)     # the accepted ones move up
     pool.trim(before + counts)                              # the others' pages are free again
+
+`path` and `counts` are chosen among the nodes whose mask is not 0.  Where the pool runs out of pages
+(`pool.missing`), the nodes without a slot then are seen by none and accepted by none, and trim leaves
+the length right; nothing of the step has to wait for the host.  A loop without a tree looks at
+`missing`, or at the slots, before it goes on: tokens without a slot are stored nowhere, and
+pool.trim(before), after the copies, takes the call back.
 
 Like the other attention operators these have no backward pass.
 """
@@ -155,7 +162,8 @@ class PagePool:
     def grow(self, cu, tokens):
         """Adds cu[b + 1] - cu[b] tokens to every sequence b, `tokens` in all (moe_pool_grow); cu [batch + 1] int32.
         Returns slots [tokens] int64 and positions [tokens] int32 of the new tokens, and the pages to copy before
-        their rows are stored, src and dst [batch] int32.  `missing` then holds how many pages were not to be had."""
+        their rows are stored, src and dst [batch] int32.  `missing` then holds how many pages were not to be had: one
+        tensor, like the pool's others, which the next call writes again."""
         return _native.pool_grow(self._at, self._index, self._on_stream(), self.ws.data_ptr(), self.ws_bytes, cu,
                                  tokens, self.missing.data_ptr())
 

@@ -128,9 +128,13 @@ size_t moe_pool_workspace_size(const moe_page_pool* pool);
  *              or of no sequence
  *   positions  [tokens] int32 receives their positions (0 of no sequence)
  *   src, dst   [batch] int32 receive each sequence's copy, or -1 and -1
- *   missing    [1] int32 receives how many pages were wanted and not free:
- *              the last ones wanted, whose entries stay -1 (a shared page
- *              stays where it is, and tokens on it get slot -1)  */
+ *   missing    [1] int32 receives how many pages were wanted and not free: the last ones
+ *              wanted, whose entries stay -1
+ * Where pages are missing, a sequence whose copy is among them does not grow: its length and its
+ * entries stay, and all its tokens get slot -1.  The others are as long as with their pages; their
+ * tokens without one get slot -1, and no attention keeps them.  A drafted node
+ * without a slot has to be an empty place (mask 0) and must not be accepted; moe_pool_trim to
+ * the lengths from before, after the copies, takes a call back. */
 moe_status moe_pool_grow(const moe_page_pool* pool, int64_t tokens, const int32_t* cu,
                          int64_t* slots, int32_t* positions, int32_t* src, int32_t* dst,
                          int32_t* missing, void* ws, size_t ws_bytes, void* stream);

@@ -79,7 +79,8 @@ class Pool:
     def grow(self, counts):
         """Returns slots, positions, (src, dst) of each sequence, and how many pages were missing.  Where all holders of
         a partly filled page grow, the one with the most tokens on it keeps it (of equals the first): what it writes
-        there is behind the others' tokens, whether their copies are to be had or not."""
+        there is behind the others' tokens, whether their copies are to be had or not.  A sequence whose copy is not to
+        be had does not grow: its new rows would have to lie among the keeper's."""
         size, cap = self.page_size, self.width * self.page_size
         free = iter([p for p, n in enumerate(self.refs) if n == 0])
         longer = [min(n + c, cap) for n, c in zip(self.lens, counts)]
@@ -116,7 +117,7 @@ class Pool:
                     page = -1
                 slots.append(page * size + pos % size if 0 <= page < len(self.refs) else -1)
                 positions.append(pos)
-            self.lens[b] = m
+            self.lens[b] = n if lost else m
         return slots, positions, pairs, missing
 
     def fork(self, parents):

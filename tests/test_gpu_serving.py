@@ -899,3 +899,85 @@ def test_pool_short_of_pages_follows_the_oracle(pages, seed):
             want.trim(lens)
         assert _state(pool) == tuple(_as_pool(want))
     assert short > 0
+
+
+def _short_pool(pages, hkv, dim, rng):
+    """Sequences of 20, 18 and 9 tokens, the second a fork of the first on the same two pages, in a pool without a free
+    page; their cache and what it holds."""
+    pool, _ = _nearly_full(pages, 3, 4, [3, 4, pages - 1])
+    cache = moe.KVCache.empty(pages, 16, hkv, dim)
+    kv = _vals(rng, 29, 2, hkv, dim)
+    slots, _, _, _ = pool.grow(dev(_cu([20, 0, 9])), 29)
+    d = dev_bf16(kv)
+    moe.kv_append(cache, d[:, 0], d[:, 1], slots)
+    pool.fork(dev(np.array([0, 0, 2], np.int32)))
+    pool.trim(dev(np.array([20, 18, 9], np.int32)))
+    return pool, cache, [kv[:20], kv[:18], kv[20:]]
+
+
+def _rows_of(cache, pool, b, n):
+    """Keys and values of a sequence's first n tokens, as whole numbers."""
+    at = torch.arange(n, device="cuda")
+    page = pool.table[b].long()[at // 16]
+    return np.stack([host(x[page, :, at % 16].contiguous()) for x in (cache.k, cache.v)], 1)
+
+
+@pytest.mark.parametrize("pages", [40, 70000])
+def test_a_step_short_of_pages_leaves_the_others_alone(pages):
+    rng = np.random.default_rng(pages)
+    hq, hkv, dim, nodes = 4, 2, 64, 5
+    pool, cache, history = _short_pool(pages, hkv, dim, rng)
+    attend = moe.TreeAttention(cache, 3, hq, nodes)
+    for turn in range(2):                    # the second time there are pages
+        before = pool.lens.clone()
+        parents = np.array([[-1, 0, 0, 1, 3]] * 3, np.int32)
+        masks, _ = moe.tree_masks(dev(parents))
+        slots, _, src, dst = pool.grow(dev(_cu([nodes] * 3)), 3 * nodes)
+        missing = pool.missing.item()
+        masks = masks * (slots >= 0).view_as(masks)
+        moe.kv_copy_pages(cache, src, dst)
+        kv, q = _vals(rng, 3 * nodes, 2, hkv, dim), _vals(rng, 3 * nodes, hq, dim)
+        d = dev_bf16(kv)
+        moe.kv_append(cache, d[:, 0], d[:, 1], slots)
+        out, lse = attend(dev_bf16(q), pool.table, before, masks, want_lse=True)
+        torch.cuda.synchronize()
+        held = [True, turn == 1, True]
+        assert missing == 1 - turn
+        assert [n - len(h) for n, h in zip(pool.lens.tolist(), history)] == [nodes * x for x in held]
+        bits, parts = serving.tree_masks(parents.tolist())[0], []
+        for b in range(3):
+            rows = np.concatenate([history[b], kv[b * nodes:(b + 1) * nodes]])
+            k, v = (_f(rows[:, i]).swapaxes(0, 1) for i in range(2))
+            keep = serving.tree_keep(bits[b] if held[b] else [0] * nodes, len(history[b]), nodes)
+            parts.append(serving.attend(_f(q[b * nodes:(b + 1) * nodes]), k, v, keep, dim ** -0.5))
+        _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)
+        path, counts = [0, 1, 3, 4, -1], [4, 4 * turn, 4]        # of the nodes whose mask is not 0
+        moe.kv_compact(cache, pool.table, before, dev(np.array([path] * 3, np.int32)), dev(np.array(counts, np.int32)))
+        pool.trim(before + dev(np.array(counts, np.int32)))
+        for b in range(3):
+            history[b] = np.concatenate([history[b], kv[[b * nodes + i for i in path[:counts[b]]]]])
+            assert pool.lens[b].item() == len(history[b])
+            assert np.array_equal(_rows_of(cache, pool, b, len(history[b])), history[b])
+        pool.refs[7:9] = 0                   # two pages become free
+
+
+@pytest.mark.parametrize("pages", [40, 70000])
+def test_tokens_short_of_pages_see_no_other_sequences_rows(pages):
+    # a token each: the fork, whose copy is not to be had, stays as it is and attends its own rows
+    rng = np.random.default_rng(pages)
+    hq, hkv, dim = 4, 2, 64
+    pool, cache, history = _short_pool(pages, hkv, dim, rng)
+    slots, _, src, dst = pool.grow(dev(_cu([1, 1, 1])), 3)
+    moe.kv_copy_pages(cache, src, dst)
+    kv, q = _vals(rng, 3, 2, hkv, dim), _vals(rng, 3, hq, dim)
+    d = dev_bf16(kv)
+    moe.kv_append(cache, d[:, 0], d[:, 1], slots)
+    out, lse = moe.attn_decode(dev_bf16(q), cache, pool.table, pool.lens, want_lse=True)
+    torch.cuda.synchronize()
+    assert slots[1].item() == -1 and pool.missing.item() == 1 and pool.lens.tolist() == [21, 18, 10]
+    parts = []
+    for b in range(3):
+        rows = history[b] if b == 1 else np.concatenate([history[b], kv[b:b + 1]])
+        k, v = (_f(rows[:, i]).swapaxes(0, 1) for i in range(2))
+        parts.append(attention.attend(_f(q[b:b + 1]), k, v, len(rows) - 1, dim ** -0.5))
+    _check(out, lse, tuple(np.concatenate(x) for x in zip(*parts)), dim)

@@ -156,3 +156,55 @@ def test_pool_short_of_pages_keeps_what_sequences_hold(seed, pages):
                 if token is not None and page >= 0:
                     assert rows[page * 16 + j % 16] == token
     assert short > 0
+
+
+def test_a_sequence_whose_copy_is_refused_stays_as_it_is():
+    p = serving.Pool(4, 16, 2, 4)
+    p.refs[2:] = [1, 1]                                   # pages of somebody else
+    p.grow([20, 0])
+    p.fork([0, 0])
+    slots, _, pairs, missing = p.grow([1, 30])
+    assert slots == [20] + [-1] * 30 and pairs == [(-1, -1)] * 2 and missing == 3
+    assert p.lens == [21, 20] and p.table == [[0, 1, -1, -1]] * 2 and p.refs == [2, 2, 1, 1]
+    p.refs[3] = 0
+    slots, _, pairs, missing = p.grow([0, 1])             # now there is a page for its copy
+    assert slots == [3 * 16 + 4] and pairs == [(-1, -1), (1, 3)] and missing == 0 and p.lens == [21, 21]
+
+
+@pytest.mark.parametrize("pages", [10, 14])
+@pytest.mark.parametrize("seed", range(8))
+def test_sequences_see_no_rows_but_their_own(seed, pages):
+    """While pages run out: a token in a sequence's length is on no page, or on one whose row holds it."""
+    rng = random.Random(7000 + 100 * pages + seed)
+    p = serving.Pool(pages, 16, 5, 6)
+    rows, story = {}, [[] for _ in range(5)]
+    for turn in range(80):
+        act = rng.choice(["grow", "grow", "fork", "cut"])
+        if act == "grow":
+            counts = [rng.choice([1, 2, 5, 20])] * 5 if rng.random() < 0.7 else [rng.choice([0, 1, 20]) for _ in range(5)]
+            before = list(p.lens)
+            slots, _, pairs, _ = p.grow(counts)
+            for a, z in pairs:
+                for r in range(16):
+                    if a >= 0:
+                        rows[z * 16 + r] = rows.get(a * 16 + r)
+            at = 0
+            for b, c in enumerate(counts):
+                for i in range(c):
+                    if slots[at] >= 0:
+                        rows[slots[at]] = (turn, b, i)
+                    at += 1
+                story[b] += [(turn, b, i) for i in range(p.lens[b] - before[b])]
+        elif act == "fork":
+            parents = [rng.choice([b, rng.randint(-1, 4)]) for b in range(5)]
+            p.fork(parents)
+            story = [list(story[x]) if x >= 0 else [] for x in parents]
+        else:
+            lens = [max(0, n - rng.choice([0, 0, 1, 3, 7, 12, 40])) for n in p.lens]
+            p.trim(lens)
+            story = [s[:n] for s, n in zip(story, lens)]
+        for b, s in enumerate(story):
+            assert len(s) == p.lens[b]
+            for j, token in enumerate(s):
+                page = p.table[b][j // 16]
+                assert page < 0 or rows[page * 16 + j % 16] == token
