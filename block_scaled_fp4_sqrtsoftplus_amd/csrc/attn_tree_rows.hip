@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
   // (32 keys a step and five tiles take as long as 64 and two.  512-element heads two steps ahead
   // spilled 30 registers: 202 us instead of 168 at 16 nodes of 64 heads.)
   constexpr int KB = ONE ? 3 : FP8 || SPLIT == 2 ? 2 : 2 * (RG / 4) * (D == 64 ? 2 : 1);
-  constexpr int DIST = SPLIT == 2 ? 1 : !FP8 ? KB - 1 : RG == 8 && D < 256 ? 2 : 1;
+  constexpr int DIST = SPLIT == 2 ? 1 : !FP8 ? KB - 1 : D < 256 ? 2 : 1;
   constexpr int SETS = FP8 ? DIST : 1;
   constexpr int TB = BN * D * 2;             // bytes of one tile
   constexpr int V0 = ONE ? 0 : KB * TB;      // the tiles of V
@@ -770,6 +770,9 @@ namespace {
 // 85 us (bf16 90) and 95 with four (95), 64 elements 61 (62) and 67 (63).  Up to 128 rows four hold
 // them all, but with 256 elements in FP8 a thread of four groups holds twice the codes of one
 // of eight and spills them: 32 nodes of 16 sequences 174 us with eight groups, 337 with four (bf16 182 and 157).
+// FP8 heads of 64 and 128 elements take eight too: a memory fault was reported the first time that four groups
+// ran on FP8 heads of 64.  Executed on the CPU, the code of that kernel stays in bounds, waits for all it
+// reads and gives the right numbers, so that the fault has no explanation, and the kernel is not there any more.
 struct TreePlan {
   int rows, rg, rgroups, pieces;   // rg: groups of 32 rows in a workgroup
   int64_t slots;
@@ -777,7 +780,7 @@ struct TreePlan {
 TreePlan tree_plan(const moe_attn_config& c, bool f8) {
   TreePlan t;
   t.rows = c.q_len * (c.heads_q / c.heads_kv);
-  t.rg = c.head_dim < 512 && (t.rows > 128 || (c.head_dim == 256 && f8)) ? 8 : 4;
+  t.rg = c.head_dim < 512 && (t.rows > 128 || f8) ? 8 : 4;
   t.rgroups = (t.rows + 32 * t.rg - 1) / (32 * t.rg);
   const int64_t per = (int64_t)c.heads_kv * t.rgroups;
   // workgroups that the GPU holds at once: two on a CU, of eight waves one
@@ -829,10 +832,9 @@ hipError_t launch_tree_rows(const moe_attn_config& c, int sinks, const moe_rows&
   hipLaunchKernelGGL((attn_tree_rows_kernel<D, F, O, G>), grid, dim3(64 * G * (D == 512 ? 2 : 1)), 0, st, a)
 #define MOE_TREE(D)                                                                            \
   case D:                                                                                      \
-    if (f8) { if (t.rg == 8) MOE_TREE_ROWS(D, true, false, 8);                                 \
-      else MOE_TREE_ROWS(D, true, false, D == 256 ? 8 : 4); }                                  \
-    else { if (t.rg == 8) MOE_TREE_ROWS(D, false, false, 8);                                   \
-      else MOE_TREE_ROWS(D, false, false, 4); }                                                \
+    if (f8) MOE_TREE_ROWS(D, true, false, 8);                                                  \
+    else if (t.rg == 8) MOE_TREE_ROWS(D, false, false, 8);                                     \
+    else MOE_TREE_ROWS(D, false, false, 4);                                                    \
     break;
   const hipError_t e = launch_workgroups((total + 7) / 8 * 8, [&](uint32_t first, dim3 grid) {
     a.first = first;
