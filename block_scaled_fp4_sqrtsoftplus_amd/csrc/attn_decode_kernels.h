@@ -1083,6 +1083,8 @@ int narrow_groups(const moe_attn_config& c, int64_t bytes) {
   return c.head_dim < 512 && rows > 16 && workgroups <= 512 && whole_sequences(bytes, 0, false) ? (int)groups : 0;
 }
 
+// (a template, so that sources which do not launch it hold no such kernels)
+template <bool TREE>
 hipError_t launch_join(const moe_attn_config& c, DecodeArgs a, hipStream_t st) {
 #define MOE_JOIN(D) \
   case D: hipLaunchKernelGGL((attn_decode_join_kernel<D>), grid, dim3(256), 0, st, a); break;
@@ -1163,7 +1165,7 @@ hipError_t launch_decode(const moe_attn_config& c, const moe_rows& q, const moe_
 #undef MOE_ROWS_ANY
 #undef MOE_ROWS
   if (e != hipSuccess || whole) return e;
-  return launch_join(c, a, st);
+  return launch_join<TREE>(c, a, st);
 }
 
 }  // namespace
