@@ -7,9 +7,9 @@
 // neither read nor computed, so its work does not grow with the position.
 //
 // Bound by the matrix units, as attn_prefill.hip, and by workgroups that start and end: a
-// row's keys are few.  8192 tokens, 32 heads of 128 on 8, window of 1024, 16 first tokens 166 us (790 TFLOP/s
+// row's keys are few.  8192 tokens, 32 heads of 128 on 8, window of 1024, 16 first tokens 165 us (793 TFLOP/s
 // of what the mask leaves; a window's first and last tiles and the one of the first tokens are computed whole);
-// five packed prompts 52.5 us.
+// five packed prompts 52.7 us.
 #include "attn_prefill_kernel.h"
 
 namespace moe {

@@ -13,15 +13,16 @@
 // bound.  Keys come through the block table 16 rows at a time, bf16 straight
 // into LDS, FP8 through registers, turned into bf16 once for all waves.
 //
-// Which calls: more than 64 rows to a key-value head.  32 sequences of 1000 to 4096
-// keys, 26 nodes, 32 heads of 128 on 8 take 94 us here and 149 in the kernel for few rows, 8 of
-// 6000 to 8192 keys and 64 nodes 86 and 224 (FP8 94 and 303), 4 of 2000 to 4096, 40 nodes of 64
-// elements 25 and 49, 16 of 2000 to 4096, 16 nodes of 32 heads on one 512-element head 97 and 142.
+// Which calls: more than 64 rows to a key-value head.  In a row (calls on one state, whose keys the caches
+// partly hold), 32 sequences of 1000 to 4096 keys, 26 nodes, 32 heads of 128 on 8 take 94 us here and 149 in
+// the kernel for few rows, 8 of 6000 to 8192 keys and 64 nodes 83 and 224 (FP8 81 and 303), 4 of 2000 to 4096,
+// 40 nodes of 64 elements 25 and 49, 16 of 2000 to 4096, 16 nodes of 32 heads on one 512-element head 97 and 142.
 //
 // Bound by memory up to about 100 rows (the keys once: 32 sequences, 26 nodes 6.3 TB/s
 // inside the loop), by the matrix units and what stands between their products
-// beyond: 64 nodes of 8 sequences, FP8 67 us (522 TFLOP/s), 16 nodes of 64 heads
-// on one 512-element head 149 us (525 TFLOP/s).  A part of a sequence costs a workgroup 9 us before its
+// beyond: among other calls 64 nodes of 8 sequences of 3000 to 8192, FP8 take 73 us (481 TFLOP/s), 16 nodes of
+// 64 heads on one 512-element head, 16 sequences of 2048 to 4096 155 us (506 TFLOP/s).  (Figures of
+// variants below are such cases in a row, both sides of one run.)  A part of a sequence costs a workgroup 9 us before its
 // first step (its place in the work, pages, masks, first tiles: each waits for
 // the one before) and 2 behind its last; the partial results, 100 MB in the last
 // case, are joined in 9 to 18 us.
@@ -773,6 +774,8 @@ namespace {
 // FP8 heads of 64 and 128 elements take eight too: a memory fault was reported the first time that four groups
 // ran on FP8 heads of 64.  Executed on the CPU, the code of that kernel stays in bounds, waits for all it
 // reads and gives the right numbers, so that the fault has no explanation, and the kernel is not there any more.
+// With up to 128 rows half of the waves then have none, and their products stand in the others' way: 26 nodes of
+// 32 sequences, 104 rows of 128 elements 117 us (bf16, four groups 95), 104 rows of 64 elements 31 (29).
 struct TreePlan {
   int rows, rg, rgroups, pieces;   // rg: groups of 32 rows in a workgroup
   int64_t slots;

@@ -497,7 +497,10 @@ hipError_t launch_pool_fork(const moe_page_pool& pool, const int32_t* parents, h
   if (pool.batch == 0) return hipSuccess;
   const PoolArgs a = pool_args(pool);
   // columns a workgroup owns: one for large batches, whose entries are its threads' registers
-  // (256 sequences: 5.8 us with an entry a thread, 11.6 with four)
+  // (256 sequences: 5.8 us with an entry a thread, 11.6 with four).  A column is one workgroup's, since
+  // all of it has to be read before any of it is written and a call has no memory of its own for the old
+  // entries; past 16384 sequences a thread holds up to 64 entries, more than its registers (570
+  // are spilled): 64 columns of 16384 sequences 47 us, of 65536 288.
   const int cols = std::clamp(kThreads / pool.batch, 1, 64);
   const unsigned groups = (unsigned)((pool.width + cols - 1) / cols) + 1;
   const int64_t most = (int64_t)pool.batch * cols;
