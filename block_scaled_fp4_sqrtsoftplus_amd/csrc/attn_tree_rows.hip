@@ -15,12 +15,12 @@
 //
 // Which calls: more than 64 rows to a key-value head.  In a row (calls on one state, whose keys the caches
 // partly hold), 32 sequences of 1000 to 4096 keys, 26 nodes, 32 heads of 128 on 8 take 94 us here and 149 in
-// the kernel for few rows, 8 of 6000 to 8192 keys and 64 nodes 83 and 224 (FP8 81 and 303), 4 of 2000 to 4096,
+// the kernel for few rows, 8 of 6000 to 8192 keys and 64 nodes 83 and 224 (FP8 83 and 303), 4 of 2000 to 4096,
 // 40 nodes of 64 elements 25 and 49, 16 of 2000 to 4096, 16 nodes of 32 heads on one 512-element head 97 and 142.
 //
 // Bound by memory up to about 100 rows (the keys once: 32 sequences, 26 nodes 6.3 TB/s
 // inside the loop), by the matrix units and what stands between their products
-// beyond: among other calls 64 nodes of 8 sequences of 3000 to 8192, FP8 take 73 us (481 TFLOP/s), 16 nodes of
+// beyond: among other calls 64 nodes of 8 sequences of 3000 to 8192, FP8 take 73 us (479 TFLOP/s), 16 nodes of
 // 64 heads on one 512-element head, 16 sequences of 2048 to 4096 155 us (506 TFLOP/s).  (Figures of
 // variants below are such cases in a row, both sides of one run.)  A part of a sequence costs a workgroup 9 us before its
 // first step (its place in the work, pages, masks, first tiles: each waits for
@@ -469,9 +469,13 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
     q_arrived();
     step_barrier<0>();
     int buf = 0, free = KB - 1;               // the tile that is read, and that of the step before it
+    // FP8's eight groups with up to 128 rows: waves without rows keep out of the others' way (26 nodes
+    // of 32 sequences, 104 rows of 128 elements: 93 us, with their products 117)
+    const bool busy = !FP8 || rg * BM + wave * 32 < p.rows;
     auto step = [&](int it, int set) __attribute__((always_inline)) {
       const int at0 = first + it * BN;
       if (it + DIST < steps) ask(DIST, free, at0 + DIST * BN, set);
+      if (busy) {
       int ka = buf * TB + k_lane(), va = V0 + buf * TB + v_lane();
       asm volatile("" : "+v"(ka), "+v"(va));
       f32x16 sc[NK];
@@ -505,6 +509,7 @@ __global__ __launch_bounds__(64 * RG * (D == 512 ? 2 : 1), 2) void attn_tree_row
         __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_s_setprio(0);
+      }
       if (it + 1 < steps) {
         put(0, buf ^ 1, (set + 1) % SETS);
         put(1, buf ^ 1, (set + 1) % SETS);
@@ -774,8 +779,8 @@ namespace {
 // FP8 heads of 64 and 128 elements take eight too: a memory fault was reported the first time that four groups
 // ran on FP8 heads of 64.  Executed on the CPU, the code of that kernel stays in bounds, waits for all it
 // reads and gives the right numbers, so that the fault has no explanation, and the kernel is not there any more.
-// With up to 128 rows half of the waves then have none, and their products stand in the others' way: 26 nodes of
-// 32 sequences, 104 rows of 128 elements 117 us (bf16, four groups 95), 104 rows of 64 elements 31 (29).
+// With up to 128 rows half of the waves then have none, and load and convert only: 26 nodes of 32 sequences,
+// 104 rows of 128 elements 93 us (bf16, four groups 95).
 struct TreePlan {
   int rows, rg, rgroups, pieces;   // rg: groups of 32 rows in a workgroup
   int64_t slots;
